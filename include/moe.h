@@ -43,7 +43,7 @@
  *     device wait that ran out, an expert-parallel row past its receive buffer) are
  *     recorded in the workspace's status word and reported by moe_check_device_error().  moe_last_error() gives a message for the last failure
  *     on the calling thread.
- *   - Inputs are finite; NaN and Inf inputs give unspecified results.
+ *   - Inputs are finite; NaN and Inf inputs give unspecified results, except where a call says.
  */
 #ifndef MOE_B200_MOE_H
 #define MOE_B200_MOE_H
@@ -549,6 +549,111 @@ moe_status_t moe_pick_rank_counts(const moe_config_t* cfg, const int32_t* topk_i
 moe_status_t moe_layer_forward(const moe_config_t* cfg, const moe_layer_inputs_t* in,
                                const moe_layer_buffers_t* bufs, void* ws, size_t ws_bytes,
                                void* stream);
+
+/* ---------------------------------------------------------------- 8-bit floating point
+ *
+ * The expert FFN with weights and activations in e4m3 and one fp32 scale for each block of
+ * 128: half the bytes of bf16 weights to store and to read (a decode step is bound by them)
+ * and twice the tensor cores' rate.  The pages have no counterpart; the stages around it are
+ * the layer's own.
+ *
+ *   rows      x [rows, cols] -> q [rows, cols] e4m3, scale [rows, ceil(cols / 128)] fp32:
+ *             a block is 128 columns of a row (the last one may be partly filled)
+ *   weights   w [E, N, K] -> q [E, N, K] e4m3, scale [E, ceil(N / 128), ceil(K / 128)] fp32:
+ *             a block is 128 x 128 entries of an expert's weight
+ *   A block with largest magnitude m, taken as at least 2^-100, has scale = m / 448 (fp32) and
+ *   q = the e4m3 number nearest to 448 x / m (the quotient taken exactly, ties to even), so an
+ *   entry stands for q * scale.  These calls define NaN and infinities: a block that holds one
+ *   gets scale NaN and NaN in every entry.
+ *
+ * Row widths (cols, K, d_model, d_ff) are multiples of 16 up to 2^24; pointers are 16-byte
+ * aligned.  dtype is the element type of x or w (MOE_F32 or MOE_BF16). */
+
+/* Rows in place: q and scale of row r in row r.  rows = 0 does nothing.  One kernel. */
+moe_status_t moe_fp8_quantize_rows(int32_t dtype, int64_t rows, int64_t cols, const void* x,
+                                   void* q, float* scale, void* stream);
+
+/* moe_dispatch's permuted copy in e4m3: each token's row is quantised once and written to
+ * rows assign_row[t, j] of x_q [max_rows, d_model] and x_scale [max_rows,
+ * ceil(d_model / 128)].  assign_row is moe_dispatch's output (called with x_perm NULL); an
+ * entry outside [0, max_rows) is a dropped pick; rows that no pick has are left as they were.
+ * x has cfg's dtype.  One kernel. */
+moe_status_t moe_fp8_permute_rows(const moe_config_t* cfg, const void* x,
+                                  const int32_t* assign_row, void* x_q, float* x_scale,
+                                  void* stream);
+
+/* Expert weights, once at load: E in 1..256, N in 1..2^24.  One kernel. */
+moe_status_t moe_fp8_quantize_weights(int32_t dtype, int64_t E, int64_t N, int64_t K,
+                                      const void* w, void* q, float* scale, void* stream);
+
+/* Workspace of the two calls below: one size whatever the problem, for the current device.
+ * Initialise it once after allocating (and again after MOE_ERR_TIMEOUT).  Its status word is
+ * read by moe_check_device_error.  Calls on one workspace must not overlap: give each stream
+ * and each captured graph that may run beside another its own. */
+moe_status_t moe_fp8_workspace_size(size_t* bytes);
+moe_status_t moe_fp8_workspace_init(void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Ragged expert buckets times their expert's weight: for each e and each row r in
+ * [seg_start[e], seg_start[e] + seg_count[e]) and n < N
+ *   out[r, n] = sum over blocks b of a_scale[r, b] * w_scale[e, n / 128, b] *
+ *               (sum over c in block b of a_q[r, c] * w_q[e, n, c])
+ * summed in fp32, out [rows, N] bf16.  a_q [rows, K], w_q [E, N, K]; seg_start, seg_count [E]
+ * int32 device arrays (moe_dispatch's expert_offsets and kept_counts, or any others; E = 1 is
+ * a plain product).  Rows outside every bucket are neither read nor written; buckets must not
+ * overlap.  A bucket that reaches outside [0, rows) is skipped and reported by
+ * moe_check_device_error as MOE_ERR_DEVICE_DATA.  N is a multiple of 8.  rows = 0 does
+ * nothing.  The order of every sum is fixed by the sizes and the buckets: equal inputs give
+ * equal bits.
+ */
+moe_status_t moe_fp8_grouped_gemm(int32_t E, int64_t rows, int64_t N, int64_t K, const void* a_q,
+                                  const float* a_scale, const int32_t* seg_start,
+                                  const int32_t* seg_count, const void* w_q,
+                                  const float* w_scale, void* out, void* ws, size_t ws_bytes,
+                                  void* stream);
+
+/* The quantised weights of a layer's experts (device pointers), as moe_fp8_quantize_weights
+ * makes them. */
+typedef struct moe_fp8_experts {
+  const void* w_gate;       /* [E, d_ff, d_model] e4m3 */
+  const float* gate_scale;  /* [E, ceil(d_ff / 128), ceil(d_model / 128)] */
+  const void* w_up;         /* [E, d_ff, d_model] e4m3 */
+  const float* up_scale;
+  const void* w_down;       /* [E, d_model, d_ff] e4m3 */
+  const float* down_scale;  /* [E, ceil(d_model / 128), ceil(d_ff / 128)] */
+} moe_fp8_experts_t;
+
+/*
+ * moe_expert_ffn on quantised rows and weights: for each bucket row r
+ *   h = silu(x[r] . w_gate[e]^T) * (x[r] . w_up[e]^T)  in fp32, then quantised as a row:
+ *   h_q [max_rows, d_ff] e4m3, h_scale [max_rows, ceil(d_ff / 128)] fp32
+ *   y_perm[r, :] = h[r] . w_down[e]^T                   [max_rows, d_model] bf16
+ * products as in moe_fp8_grouped_gemm.  Here 448 h / m is rounded to fp32 before it is
+ * rounded to e4m3 (h itself is an fp32 sum).  bf16 layers only (MOE_ERR_UNSUPPORTED
+ * otherwise).  x_q, x_scale: moe_fp8_permute_rows' outputs.
+ */
+moe_status_t moe_expert_ffn_fp8(const moe_config_t* cfg, const void* x_q, const float* x_scale,
+                                const int32_t* expert_offsets, const int32_t* kept_counts,
+                                const moe_fp8_experts_t* experts, void* h_q, float* h_scale,
+                                void* y_perm, void* ws, size_t ws_bytes, void* stream);
+
+/* Intermediates of moe_layer_forward_fp8 (device pointers, caller-allocated). */
+typedef struct moe_fp8_buffers {
+  void* x_q;       /* [max_rows, d_model] e4m3 */
+  float* x_scale;  /* [max_rows, ceil(d_model / 128)] */
+  void* h_q;       /* [max_rows, d_ff] e4m3 */
+  float* h_scale;  /* [max_rows, ceil(d_ff / 128)] */
+} moe_fp8_buffers_t;
+
+/* moe_layer_forward with the experts in 8-bit floating point: route, dispatch without a
+ * permuted copy, moe_fp8_permute_rows, moe_expert_ffn_fp8, combine, statistics.  in->w_gate,
+ * w_up, w_down and bufs->x_perm, h are not read.  ws as for moe_layer_forward, fp8_ws as for
+ * moe_expert_ffn_fp8; check both with moe_check_device_error. */
+moe_status_t moe_layer_forward_fp8(const moe_config_t* cfg, const moe_layer_inputs_t* in,
+                                   const moe_fp8_experts_t* experts,
+                                   const moe_layer_buffers_t* bufs,
+                                   const moe_fp8_buffers_t* fp8_bufs, void* ws, size_t ws_bytes,
+                                   void* fp8_ws, size_t fp8_ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------- errors */
 

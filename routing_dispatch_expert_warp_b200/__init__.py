@@ -279,13 +279,14 @@ class LayerBuffers:
     assign_row: torch.Tensor
     token_of_row: torch.Tensor
     x_perm: Optional[torch.Tensor]   # None: the gate/up GEMM gathers rows of x
-    h: torch.Tensor
+    h: Optional[torch.Tensor]        # None: the layer keeps its hidden rows elsewhere (fp8)
     y_perm: torch.Tensor
     out: torch.Tensor
     stats: torch.Tensor
 
     @staticmethod
-    def allocate(cfg: MoeConfig, device="cuda", gather: bool = False) -> "LayerBuffers":
+    def allocate(cfg: MoeConfig, device="cuda", gather: bool = False,
+                 hidden: bool = True) -> "LayerBuffers":
         T, d, f, E, k = cfg.T, cfg.d_model, cfg.d_ff, cfg.E, cfg.k
         R = max_rows(cfg)
         dt = torch.float32 if cfg.dtype == F32 else torch.bfloat16
@@ -298,7 +299,7 @@ class LayerBuffers:
             expert_offsets=torch.empty(E + 1, **i32), assign_row=torch.empty((T, k), **i32),
             token_of_row=torch.empty(max(R, 1), **i32),
             x_perm=None if gather else torch.empty((max(R, 1), d), dtype=dt, device=device),
-            h=torch.empty((max(R, 1), f), dtype=dt, device=device),
+            h=torch.empty((max(R, 1), f), dtype=dt, device=device) if hidden else None,
             y_perm=torch.empty((max(R, 1), d), dtype=dt, device=device),
             out=torch.empty((T, d), dtype=dt, device=device),
             stats=stats_buffer(device))
@@ -436,3 +437,8 @@ class HostPipeline:
         if n:
             comp.wait_event(fetched[-1])
 
+
+from . import fp8  # noqa: E402  (needs the names above)
+from .fp8 import *  # noqa: E402,F401,F403
+
+__all__ += fp8.__all__

@@ -57,6 +57,15 @@ class MoeLayerBuffers(ctypes.Structure):
                 ("y_perm", c_vp), ("out", c_vp), ("stats", c_vp)]
 
 
+class MoeFp8Experts(ctypes.Structure):
+    _fields_ = [("w_gate", c_vp), ("gate_scale", c_vp), ("w_up", c_vp), ("up_scale", c_vp),
+                ("w_down", c_vp), ("down_scale", c_vp)]
+
+
+class MoeFp8Buffers(ctypes.Structure):
+    _fields_ = [("x_q", c_vp), ("x_scale", c_vp), ("h_q", c_vp), ("h_scale", c_vp)]
+
+
 class MoeEpConfig(ctypes.Structure):
     _fields_ = [("world", c_i32), ("rank", c_i32), ("ranks_per_node", c_i32),
                 ("n_local", c_i32), ("expert_rank", c_vp), ("recv_rows", c_i64)]
@@ -120,6 +129,18 @@ PROTOTYPES = {
                                      P(MoeLoadStats), c_vp]),
     "moe_layer_forward": (c_i32, [P(MoeConfig), P(MoeLayerInputs), P(MoeLayerBuffers), c_vp,
                                   c_sz, c_vp]),
+    "moe_fp8_quantize_rows": (c_i32, [c_i32, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp]),
+    "moe_fp8_permute_rows": (c_i32, [P(MoeConfig), c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "moe_fp8_quantize_weights": (c_i32, [c_i32, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp]),
+    "moe_fp8_workspace_size": (c_i32, [P(c_sz)]),
+    "moe_fp8_workspace_init": (c_i32, [c_vp, c_sz, c_vp]),
+    "moe_fp8_grouped_gemm": (c_i32, [c_i32, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                     c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "moe_expert_ffn_fp8": (c_i32, [P(MoeConfig), c_vp, c_vp, c_vp, c_vp, P(MoeFp8Experts), c_vp,
+                                   c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "moe_layer_forward_fp8": (c_i32, [P(MoeConfig), P(MoeLayerInputs), P(MoeFp8Experts),
+                                      P(MoeLayerBuffers), P(MoeFp8Buffers), c_vp, c_sz, c_vp,
+                                      c_sz, c_vp]),
     "moe_static_scratch_check": (c_i32, [c_vp]),
     "moe_check_device_error": (c_i32, [c_vp, c_sz, c_vp]),
     "moe_last_error": (ctypes.c_char_p, []),

@@ -678,6 +678,9 @@ moe_status_t device_error_status(const DevStatus& h) {
     return fail(MOE_ERR_DEVICE_DATA,
                 "expert-parallel row past the receive buffer's recv_rows (pick %llu)",
                 (unsigned long long)h.info);
+  if (h.code == DEV_BAD_BUCKET)
+    return fail(MOE_ERR_DEVICE_DATA, "fp8 product: bucket %llu reaches outside the rows",
+                (unsigned long long)h.info);
   return fail(MOE_ERR_DEVICE_DATA, "invalid expert index in topk_idx (flat index %llu)",
               (unsigned long long)h.info);
 }
@@ -900,6 +903,256 @@ moe_status_t moe_selftest_bounded_wait(void* ws, size_t ws_bytes, void* stream) 
                                          static_cast<cudaStream_t>(stream));
   if (err != cudaSuccess) return cuda_fail(err, "moe_selftest_bounded_wait launch");
   return MOE_OK;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ 8-bit floating point
+namespace {
+
+constexpr int64_t kMaxWidth = 1LL << 24;
+
+moe_status_t check_fp8_width(const char* name, const char* what, int64_t v) {
+  MOE_REQUIRE(v >= 16 && v <= kMaxWidth && v % 16 == 0,
+              "%s: %s must be a multiple of 16 in [16, 2^24] (got %lld)", name, what,
+              (long long)v);
+  return MOE_OK;
+}
+
+moe_status_t check_fp8_dtype(const char* name, int32_t dtype) {
+  MOE_REQUIRE(dtype == MOE_F32 || dtype == MOE_BF16, "%s: unknown dtype %d", name, dtype);
+  return MOE_OK;
+}
+
+moe_status_t check_fp8_ws(const char* name, const void* ws, size_t ws_bytes) {
+  MOE_REQUIRE(ws != nullptr, "%s: workspace is NULL", name);
+  MOE_REQUIRE((reinterpret_cast<uintptr_t>(ws) & (kWsAlign - 1)) == 0,
+              "%s: workspace must be 256-byte aligned", name);
+  if (ws_bytes < fp8_workspace_bytes())
+    return fail(MOE_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", name, ws_bytes,
+                fp8_workspace_bytes());
+  return MOE_OK;
+}
+
+// Tiles are numbered in 32 bits.
+moe_status_t check_fp8_tiles(const char* name, int64_t E, int64_t rows, int64_t N) {
+  if ((rows / 128 + E) * ((N + 127) / 128) > 2147483647LL)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^31 output tiles", name);
+  return MOE_OK;
+}
+
+moe_status_t run_fp8_gemm(const char* name, const Fp8Gemm& g, void* ws, void* stream) {
+  const char* why = "";
+  cudaError_t err =
+      launch_fp8_gemm(g, ws, g_wait_ns.load(), static_cast<cudaStream_t>(stream), &why);
+  if (err != cudaSuccess) {
+    if (why[0]) return fail(MOE_ERR_CUDA, "%s: %s", name, why);
+    return cuda_fail(err, name);
+  }
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_fp8_quantize_rows(int32_t dtype, int64_t rows, int64_t cols, const void* x,
+                                   void* q, float* scale, void* stream) {
+  const char* name = "moe_fp8_quantize_rows";
+  moe_status_t st;
+  if ((st = check_fp8_dtype(name, dtype)) != MOE_OK) return st;
+  MOE_REQUIRE(rows >= 0 && rows <= 2147483647LL, "%s: rows must be in [0, 2^31)", name);
+  if ((st = check_fp8_width(name, "cols", cols)) != MOE_OK) return st;
+  if (rows == 0) return MOE_OK;
+  MOE_REQUIRE(x && q && scale, "%s: NULL pointer", name);
+  MOE_REQUIRE(aligned16(x) && aligned16(q) && aligned16(scale),
+              "%s: tensors must be 16-byte aligned", name);
+  cudaError_t err = launch_fp8_quantize_rows(dtype, x, rows, cols, nullptr, 0, rows, q, scale,
+                                             static_cast<cudaStream_t>(stream));
+  if (err != cudaSuccess) return cuda_fail(err, name);
+  return MOE_OK;
+}
+
+moe_status_t moe_fp8_permute_rows(const moe_config_t* cfg, const void* x,
+                                  const int32_t* assign_row, void* x_q, float* x_scale,
+                                  void* stream) {
+  const char* name = "moe_fp8_permute_rows";
+  Shape s;
+  moe_status_t st = check_config(cfg, &s);
+  if (st != MOE_OK) return st;
+  if ((st = check_fp8_width(name, "d_model", s.d)) != MOE_OK) return st;
+  MOE_REQUIRE(x && assign_row && x_q && x_scale, "%s: NULL pointer", name);
+  MOE_REQUIRE(aligned16(x) && aligned16(assign_row) && aligned16(x_q) && aligned16(x_scale),
+              "%s: tensors must be 16-byte aligned", name);
+  cudaError_t err =
+      launch_fp8_quantize_rows(s.dtype, x, s.T, s.d, assign_row, s.k, s.max_rows, x_q, x_scale,
+                               static_cast<cudaStream_t>(stream));
+  if (err != cudaSuccess) return cuda_fail(err, name);
+  return MOE_OK;
+}
+
+moe_status_t moe_fp8_quantize_weights(int32_t dtype, int64_t E, int64_t N, int64_t K,
+                                      const void* w, void* q, float* scale, void* stream) {
+  const char* name = "moe_fp8_quantize_weights";
+  moe_status_t st;
+  if ((st = check_fp8_dtype(name, dtype)) != MOE_OK) return st;
+  MOE_REQUIRE(E >= 1 && E <= MOE_MAX_EXPERTS, "%s: E must be in [1, %d]", name, MOE_MAX_EXPERTS);
+  MOE_REQUIRE(N >= 1 && N <= kMaxWidth, "%s: N must be in [1, 2^24]", name);
+  if ((st = check_fp8_width(name, "K", K)) != MOE_OK) return st;
+  MOE_REQUIRE(w && q && scale, "%s: NULL pointer", name);
+  MOE_REQUIRE(aligned16(w) && aligned16(q) && aligned16(scale),
+              "%s: tensors must be 16-byte aligned", name);
+  cudaError_t err = launch_fp8_quantize_weights(dtype, w, E, N, K, q, scale,
+                                                static_cast<cudaStream_t>(stream));
+  if (err != cudaSuccess) return cuda_fail(err, name);
+  return MOE_OK;
+}
+
+moe_status_t moe_fp8_workspace_size(size_t* bytes) {
+  MOE_REQUIRE(bytes != nullptr, "moe_fp8_workspace_size: bytes is NULL");
+  *bytes = fp8_workspace_bytes();
+  return MOE_OK;
+}
+
+moe_status_t moe_fp8_workspace_init(void* ws, size_t ws_bytes, void* stream) {
+  moe_status_t st = check_fp8_ws("moe_fp8_workspace_init", ws, ws_bytes);
+  if (st != MOE_OK) return st;
+  cudaError_t err = cudaMemsetAsync(ws, 0, kFp8PartialsOffset, static_cast<cudaStream_t>(stream));
+  if (err != cudaSuccess) return cuda_fail(err, "moe_fp8_workspace_init");
+  return MOE_OK;
+}
+
+moe_status_t moe_fp8_grouped_gemm(int32_t E, int64_t rows, int64_t N, int64_t K, const void* a_q,
+                                  const float* a_scale, const int32_t* seg_start,
+                                  const int32_t* seg_count, const void* w_q,
+                                  const float* w_scale, void* out, void* ws, size_t ws_bytes,
+                                  void* stream) {
+  const char* name = "moe_fp8_grouped_gemm";
+  moe_status_t st;
+  MOE_REQUIRE(E >= 1 && E <= MOE_MAX_EXPERTS, "%s: E must be in [1, %d]", name, MOE_MAX_EXPERTS);
+  MOE_REQUIRE(rows >= 0 && rows <= 2147483647LL, "%s: rows must be in [0, 2^31)", name);
+  MOE_REQUIRE(N >= 8 && N <= kMaxWidth && N % 8 == 0,
+              "%s: N must be a multiple of 8 in [8, 2^24] (got %lld)", name, (long long)N);
+  if ((st = check_fp8_width(name, "K", K)) != MOE_OK) return st;
+  if ((st = check_fp8_tiles(name, E, rows, N)) != MOE_OK) return st;
+  if ((st = check_fp8_ws(name, ws, ws_bytes)) != MOE_OK) return st;
+  if (rows == 0) return MOE_OK;
+  MOE_REQUIRE(a_q && a_scale && seg_start && seg_count && w_q && w_scale && out,
+              "%s: NULL pointer", name);
+  MOE_REQUIRE(aligned16(a_q) && aligned16(a_scale) && aligned16(w_q) && aligned16(w_scale) &&
+                  aligned16(out),
+              "%s: tensors must be 16-byte aligned", name);
+  Fp8Gemm g{};
+  g.E = E;
+  g.rows = rows;
+  g.N = N;
+  g.K = K;
+  g.a = a_q;
+  g.a_scale = a_scale;
+  g.seg_start = seg_start;
+  g.seg_count = seg_count;
+  g.w0 = w_q;
+  g.w_scale0 = w_scale;
+  g.out = out;
+  return run_fp8_gemm(name, g, ws, stream);
+}
+
+moe_status_t moe_expert_ffn_fp8(const moe_config_t* cfg, const void* x_q, const float* x_scale,
+                                const int32_t* expert_offsets, const int32_t* kept_counts,
+                                const moe_fp8_experts_t* w, void* h_q, float* h_scale,
+                                void* y_perm, void* ws, size_t ws_bytes, void* stream) {
+  const char* name = "moe_expert_ffn_fp8";
+  Shape s;
+  moe_status_t st = check_config(cfg, &s);
+  if (st != MOE_OK) return st;
+  if (s.dtype != MOE_BF16)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: the layer's dtype must be bf16", name);
+  if ((st = check_fp8_width(name, "d_model", s.d)) != MOE_OK) return st;
+  if ((st = check_fp8_width(name, "d_ff", s.f)) != MOE_OK) return st;
+  if ((st = check_fp8_tiles(name, s.E, s.max_rows, s.d > s.f ? s.d : s.f)) != MOE_OK) return st;
+  if ((st = check_fp8_ws(name, ws, ws_bytes)) != MOE_OK) return st;
+  MOE_REQUIRE(w != nullptr, "%s: experts is NULL", name);
+  MOE_REQUIRE(x_q && x_scale && expert_offsets && kept_counts && h_q && h_scale && y_perm &&
+                  w->w_gate && w->gate_scale && w->w_up && w->up_scale && w->w_down &&
+                  w->down_scale,
+              "%s: NULL pointer", name);
+  MOE_REQUIRE(aligned16(x_q) && aligned16(x_scale) && aligned16(h_q) && aligned16(h_scale) &&
+                  aligned16(y_perm) && aligned16(w->w_gate) && aligned16(w->gate_scale) &&
+                  aligned16(w->w_up) && aligned16(w->up_scale) && aligned16(w->w_down) &&
+                  aligned16(w->down_scale),
+              "%s: tensors must be 16-byte aligned", name);
+  Fp8Gemm g{};
+  g.E = s.E;
+  g.rows = s.max_rows;
+  g.seg_start = expert_offsets;
+  g.seg_count = kept_counts;
+  g.N = s.f;
+  g.K = s.d;
+  g.a = x_q;
+  g.a_scale = x_scale;
+  g.w0 = w->w_gate;
+  g.w_scale0 = w->gate_scale;
+  g.w1 = w->w_up;
+  g.w_scale1 = w->up_scale;
+  g.h = h_q;
+  g.h_scale = h_scale;
+  if ((st = run_fp8_gemm(name, g, ws, stream)) != MOE_OK) return st;
+  g.N = s.d;
+  g.K = s.f;
+  g.a = h_q;
+  g.a_scale = h_scale;
+  g.w0 = w->w_down;
+  g.w_scale0 = w->down_scale;
+  g.w1 = nullptr;
+  g.w_scale1 = nullptr;
+  g.h = nullptr;
+  g.h_scale = nullptr;
+  g.out = y_perm;
+  return run_fp8_gemm(name, g, ws, stream);
+}
+
+moe_status_t moe_layer_forward_fp8(const moe_config_t* cfg, const moe_layer_inputs_t* in,
+                                   const moe_fp8_experts_t* experts,
+                                   const moe_layer_buffers_t* b, const moe_fp8_buffers_t* f,
+                                   void* ws, size_t ws_bytes, void* fp8_ws, size_t fp8_ws_bytes,
+                                   void* stream) {
+  const char* name = "moe_layer_forward_fp8";
+  MOE_REQUIRE(in != nullptr && b != nullptr && f != nullptr,
+              "%s: NULL inputs or buffers", name);
+  // what a later stage would refuse is refused before anything is enqueued
+  Shape s;
+  moe_status_t st = check_config(cfg, &s);
+  if (st != MOE_OK) return st;
+  if (s.dtype != MOE_BF16)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: the layer's dtype must be bf16", name);
+  if ((st = check_fp8_width(name, "d_model", s.d)) != MOE_OK) return st;
+  if ((st = check_fp8_width(name, "d_ff", s.f)) != MOE_OK) return st;
+  if ((st = check_fp8_ws(name, fp8_ws, fp8_ws_bytes)) != MOE_OK) return st;
+  MOE_REQUIRE(f->x_q && f->x_scale && f->h_q && f->h_scale && experts && b->y_perm && b->out,
+              "%s: NULL pointer", name);
+  st = moe_route_ex(cfg, in->x, in->w_router, in->w_router_split, in->logit_bias,
+                    in->bias_row_stride, b->logits, b->topk_idx, b->topk_w, ws, ws_bytes, stream);
+  if (st != MOE_OK) return st;
+  // the logits the router wrote: the caller's array, else the workspace's
+  const float* z = b->logits;
+  if (z == nullptr)
+    z = reinterpret_cast<const float*>(static_cast<const uint8_t*>(ws) +
+                                       workspace_layout(s).logits);
+  st = moe_dispatch_scored(cfg, in->x, b->topk_idx, z, in->logit_bias, in->bias_row_stride,
+                           b->routed_counts, b->kept_counts, b->expert_offsets, b->assign_row,
+                           b->token_of_row, nullptr, ws, ws_bytes, stream);
+  if (st != MOE_OK) return st;
+  st = moe_fp8_permute_rows(cfg, in->x, b->assign_row, f->x_q, f->x_scale, stream);
+  if (st != MOE_OK) return st;
+  st = moe_expert_ffn_fp8(cfg, f->x_q, f->x_scale, b->expert_offsets, b->kept_counts, experts,
+                          f->h_q, f->h_scale, b->y_perm, fp8_ws, fp8_ws_bytes, stream);
+  if (st != MOE_OK) return st;
+  st = moe_combine(cfg, b->y_perm, b->assign_row, b->topk_w, b->out, stream);
+  if (st != MOE_OK) return st;
+  if (b->stats != nullptr)
+    st = moe_load_stats(cfg, b->routed_counts, b->kept_counts, b->assign_row, b->stats, nullptr,
+                        stream);
+  return st;
 }
 
 }  // extern "C"

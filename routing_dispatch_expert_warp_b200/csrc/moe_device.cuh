@@ -22,7 +22,8 @@ enum DevError : unsigned int {
   DEV_OK = 0,
   DEV_TIMEOUT = 1,
   DEV_BAD_EXPERT = 2,
-  DEV_RECV_OVERFLOW = 3  // an expert-parallel row would land past the receive buffer
+  DEV_RECV_OVERFLOW = 3, // an expert-parallel row would land past the receive buffer
+  DEV_BAD_BUCKET = 4     // an fp8 product's bucket reaches outside its rows
 };
 
 __device__ __forceinline__ void record_error(DevStatus* st, unsigned int code,

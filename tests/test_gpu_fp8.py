@@ -1,0 +1,507 @@
+"""The 8-bit floating point operators against their definition in 64 bits: quantisation of
+rows and weights bit by bit, ragged products and the SwiGLU FFN within the rounding that their
+arithmetic admits, and the calls around them (streams, graphs, rows outside the buckets)."""
+import numpy as np
+import pytest
+import torch
+
+import fp8_oracle as O
+import routing_dispatch_expert_warp_b200 as M
+from routing_dispatch_expert_warp_b200 import workload as W
+
+pytestmark = pytest.mark.gpu
+E4M3 = torch.float8_e4m3fn
+
+
+@pytest.fixture(autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    yield
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def codes(q):
+    return q.view(torch.uint8).cpu().numpy()
+
+
+def assert_same_scales(got, ref):
+    got = got.cpu().numpy()
+    assert got.shape == ref.shape
+    assert np.array_equal(got.view(np.uint32)[~np.isnan(ref)], ref.view(np.uint32)[~np.isnan(ref)])
+    assert np.isnan(got[np.isnan(ref)]).all()
+
+
+def assert_same_codes(got, ref):
+    got = codes(got)
+    nan = (ref & 0x7F) == 0x7F
+    assert np.array_equal(got[~nan], ref[~nan]), (got != ref).sum()
+    assert ((got[nan] & 0x7F) == 0x7F).all()
+
+
+def values(shape, dtype, seed, kind="normal"):
+    g = gen(seed)
+    x = torch.randn(shape, generator=g, dtype=torch.float64)
+    if kind == "outliers":
+        x = x * (1 + 100 * (torch.rand(shape, generator=g) < 0.01))
+    elif kind == "spread":   # magnitudes over the whole range of the type
+        x = x * torch.exp2(torch.rand(shape, generator=g) * 240 - 130)
+    elif kind == "tiny":     # blocks below the floor, subnormals among them
+        x = x * torch.exp2(torch.rand(shape, generator=g) * 60 - 150)
+    elif kind == "borders":  # short fractions: quotients on the borders of e4m3
+        x = torch.randint(-32, 33, shape, generator=g).double() / 8
+    elif kind == "zero":
+        x = torch.zeros(shape, dtype=torch.float64)
+    return x.to(dtype)
+
+
+# ------------------------------------------------------------------ rows
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(1, 16), (1, 128), (3, 144), (7, 1520), (129, 528),
+                                       (1000, 4096), (2, 16384)])
+@pytest.mark.parametrize("kind", ["normal", "outliers", "spread", "tiny", "borders", "zero"])
+def test_rows(rows, cols, dtype, kind):
+    x = values((rows, cols), dtype, rows + cols, kind)
+    q = torch.empty((rows, cols), dtype=E4M3, device="cuda")
+    s = torch.empty((rows, O.blocks(cols)), device="cuda")
+    M.moe_fp8_quantize_rows(x.cuda(), q, s)
+    ref_q, ref_s = O.quantize_rows(x)
+    assert_same_scales(s, ref_s)
+    assert_same_codes(q, ref_q)
+
+
+def test_rows_every_bf16_quotient():
+    """All pairs of significands: x / m for x, m in 128 .. 255, m the block's largest."""
+    m, x = torch.meshgrid(torch.arange(128, 256), torch.arange(128, 256), indexing="ij")
+    rows = torch.zeros((128 * 128, 16))
+    rows[:, 0] = m.flatten().float()
+    for i in range(1, 15):  # and over the exponents that reach e4m3's smallest steps
+        rows[:, i] = x.flatten().float() * 2.0 ** (-1 - i) * (-1) ** i
+    rows = rows.bfloat16()
+    q = torch.empty(rows.shape, dtype=E4M3, device="cuda")
+    s = torch.empty((rows.shape[0], 1), device="cuda")
+    M.moe_fp8_quantize_rows(rows.cuda(), q, s)
+    ref_q, ref_s = O.quantize_rows(rows)
+    assert_same_scales(s, ref_s)
+    assert_same_codes(q, ref_q)
+
+
+def test_rows_fp32_next_to_borders():
+    """fp32 entries at the fp32 numbers next to a border of e4m3, on both sides of it."""
+    g = gen(5)
+    m = (1 + torch.rand(4096, generator=g)).float()
+    border = torch.from_numpy(O.BORDERS)[torch.randint(0, 126, (4096, 15), generator=g)]
+    x = (border * m[:, None].double() / 448).float()
+    step = torch.randint(-2, 3, x.shape, generator=g, dtype=torch.int32)
+    x = (x.view(torch.int32) + step).view(torch.float32)
+    rows = torch.cat([m[:, None], x], 1)
+    q = torch.empty(rows.shape, dtype=E4M3, device="cuda")
+    s = torch.empty((rows.shape[0], 1), device="cuda")
+    M.moe_fp8_quantize_rows(rows.cuda(), q, s)
+    ref_q, ref_s = O.quantize_rows(rows)
+    assert_same_scales(s, ref_s)
+    assert_same_codes(q, ref_q)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_rows_with_nan_and_infinity(dtype):
+    x = values((6, 400), dtype, 3)
+    x[0, 5] = float("nan")
+    x[1, 130] = float("inf")
+    x[2, 399] = -float("inf")
+    x[3, 128] = float("nan")
+    x[3, 129] = float("inf")
+    q = torch.empty(x.shape, dtype=E4M3, device="cuda")
+    s = torch.empty((6, 4), device="cuda")
+    M.moe_fp8_quantize_rows(x.cuda(), q, s)
+    ref_q, ref_s = O.quantize_rows(x)
+    assert np.isnan(ref_s).sum() == 4
+    assert_same_scales(s, ref_s)
+    assert_same_codes(q, ref_q)
+
+
+def test_no_rows():
+    q = torch.empty((0, 128), dtype=E4M3, device="cuda")
+    M.moe_fp8_quantize_rows(torch.empty((0, 128), device="cuda"), q,
+                            torch.empty((0, 1), device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,d,E,k,cf", [(1, 16, 1, 1, 0.0), (1, 4096, 8, 2, 0.0),
+                                        (37, 1520, 13, 8, 0.5), (600, 656, 256, 8, 1.0),
+                                        (64, 7168, 4, 3, 0.0)])
+def test_permute_writes_the_kept_picks_rows(T, d, E, k, cf, dtype):
+    g = gen(T + d)
+    cfg = M.make_config(T, d, 128, E, k, capacity_factor=cf,
+                        dtype=M.F32 if dtype == torch.float32 else M.BF16)
+    R = M.max_rows(cfg)
+    x = values((T, d), dtype, T)
+    row = torch.full((T * k,), -1, dtype=torch.int32)
+    kept = torch.randperm(T * k, generator=g)[:max(1, min(R - 1, T * k))]
+    row[kept] = torch.randperm(R, generator=g)[:len(kept)].int()
+    row = row.view(T, k)
+    q = torch.full((R, d), 0.5, device="cuda").to(E4M3)
+    s = torch.full((R, O.blocks(d)), 7.0, device="cuda")
+    M.moe_fp8_permute_rows(cfg, x.cuda(), row.cuda(), q, s)
+    tq, ts = O.quantize_rows(x)
+    ref_q = np.full((R, d), 0x30, dtype=np.uint8)
+    ref_s = np.full((R, O.blocks(d)), 7.0, dtype=np.float32)
+    for t in range(T):
+        for r in row[t].tolist():
+            if r >= 0:
+                ref_q[r], ref_s[r] = tq[t], ts[t]
+    assert_same_scales(s, ref_s)
+    assert_same_codes(q, ref_q)
+
+
+def test_permute_skips_rows_outside_the_buffer():
+    cfg = M.make_config(4, 128, 128, 2, 2)
+    row = torch.tensor([[0, 8], [1 << 30, 1], [-5, 2], [7, -1]], dtype=torch.int32)
+    full = torch.zeros((12, 128), device="cuda").to(E4M3)
+    scale = torch.zeros((12, 1), device="cuda")
+    M.moe_fp8_permute_rows(cfg, torch.ones((4, 128), device="cuda").bfloat16(), row.cuda(),
+                           full[2:10], scale.narrow(0, 4, 8))
+    wrote = [i for i in range(12) if codes(full)[i].any()]
+    assert wrote == [2, 3, 4, 9]
+    assert (scale != 0).flatten().nonzero().flatten().tolist() == [4, 5, 6, 11]
+
+
+# ------------------------------------------------------------------ weights
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(1, 1, 16), (2, 128, 128), (3, 200, 272), (5, 129, 144),
+                                   (1, 1000, 1520), (256, 8, 16)])
+@pytest.mark.parametrize("kind", ["normal", "spread", "borders"])
+def test_weights(shape, dtype, kind):
+    w = values(shape, dtype, sum(shape), kind)
+    q = torch.empty(shape, dtype=E4M3, device="cuda")
+    s = torch.empty(M.fp8_scale_shape(shape), device="cuda")
+    M.moe_fp8_quantize_weights(w.cuda(), q, s)
+    ref_q, ref_s = O.quantize_weights(w)
+    assert_same_scales(s, ref_s)
+    assert_same_codes(q, ref_q)
+
+
+def test_weights_with_nan():
+    w = values((2, 260, 272), torch.bfloat16, 1)
+    w[1, 129, 271] = float("nan")
+    w[0, 0, 0] = float("inf")
+    q = torch.empty(w.shape, dtype=E4M3, device="cuda")
+    s = torch.empty(M.fp8_scale_shape(w.shape), device="cuda")
+    M.moe_fp8_quantize_weights(w.cuda(), q, s)
+    ref_q, ref_s = O.quantize_weights(w)
+    assert np.isnan(ref_s).sum() == 2
+    assert_same_scales(s, ref_s)
+    assert_same_codes(q, ref_q)
+
+
+# ------------------------------------------------------------------ products
+def quantized_rows(x):
+    q = torch.empty(x.shape, dtype=E4M3, device="cuda")
+    s = torch.empty(M.fp8_scale_shape(x.shape), device="cuda")
+    M.moe_fp8_quantize_rows(x.cuda(), q, s)
+    return q, s
+
+
+def quantized_weights(w):
+    q = torch.empty(w.shape, dtype=E4M3, device="cuda")
+    s = torch.empty(M.fp8_scale_shape(w.shape), device="cuda")
+    M.moe_fp8_quantize_weights(w.cuda(), q, s)
+    return q, s
+
+
+def starts(counts, gap=0):
+    at, first = 0, []
+    for c in counts:
+        first.append(at)
+        at += c + gap
+    return first, at
+
+
+GEMM = [  # counts, N, K
+    ([1], 8, 16),
+    ([1], 256, 128),
+    ([2, 0, 1], 136, 144),
+    ([128], 256, 256),
+    ([129, 127], 264, 272),
+    ([0, 0, 300, 0, 31, 33, 64, 96, 97], 1000, 1520),
+    ([64] * 3, 4096, 7168),
+    ([700, 5], 520, 2048),
+    ([1] * 256, 128, 128),
+    ([3, 0] * 128, 48, 400),
+    ([2000], 640, 128),
+    ([0, 0], 256, 256),
+    ([1, 1], 4096, 14336),
+    ([260, 513, 1, 255, 256, 257], 768, 640),
+]
+
+
+@pytest.mark.parametrize("gap", [0, 3])
+@pytest.mark.parametrize("counts,N,K", GEMM)
+def test_grouped_gemm(counts, N, K, gap):
+    g = gen(N + K)
+    E = len(counts)
+    first, rows = starts(counts, gap)
+    rows += 2  # rows behind the last bucket
+    a_q, a_s = quantized_rows(torch.randn((rows, K), generator=g).bfloat16())
+    w_q, w_s = quantized_weights(torch.randn((E, N, K), generator=g) / K ** 0.5)
+    out = torch.full((rows, N), 3.25, dtype=torch.bfloat16, device="cuda")
+    ws = M.alloc_fp8_workspace()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    M.moe_fp8_grouped_gemm(a_q, a_s, torch.tensor(first, **i32), torch.tensor(counts, **i32),
+                           w_q, w_s, out, ws)
+    M.moe_check_device_error(ws)
+    check_product(out, a_q, a_s, w_q, w_s, first, counts)
+
+
+def check_product(out, a_q, a_s, w_q, w_s, first, counts, untouched=3.25):
+    got = out.cpu().double()
+    a = O.rows_value(a_q, a_s)
+    seen = torch.zeros(len(got), dtype=torch.bool)
+    tol = O.sum_error(a.shape[1])
+    for e, (r0, c) in enumerate(zip(first, counts)):
+        if c == 0:
+            continue
+        at = slice(r0, r0 + c)
+        ref, mag = O.product(a[at], O.weight_value(w_q[e], w_s[e]))
+        room = O.BF16_HALF_STEP * ref.abs() + (1 + O.BF16_HALF_STEP) * tol * mag
+        assert ((got[at] - ref).abs() <= room).all(), (e, (got[at] - ref).abs().max())
+        seen[at] = True
+    assert (got[~seen] == untouched).all()
+
+
+def test_grouped_gemm_equal_calls_give_equal_bits_and_streams_do_not_matter():
+    counts, N, K = [5, 0, 130, 1], 1000, 2064
+    first, rows = starts(counts)
+    g = gen(1)
+    a_q, a_s = quantized_rows(torch.randn((rows, K), generator=g))
+    w_q, w_s = quantized_weights(torch.randn((4, N, K), generator=g))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    f, c = torch.tensor(first, **i32), torch.tensor(counts, **i32)
+    outs = []
+    torch.cuda.synchronize()
+    for stream in (None, None, torch.cuda.Stream(), torch.cuda.Stream()):
+        out = torch.zeros((rows, N), dtype=torch.bfloat16, device="cuda")
+        torch.cuda.synchronize()
+        ws = M.alloc_fp8_workspace(stream=stream)
+        for _ in range(3):
+            M.moe_fp8_grouped_gemm(a_q, a_s, f, c, w_q, w_s, out, ws, stream)
+        outs.append(out)
+    torch.cuda.synchronize()
+    for out in outs[1:]:
+        assert torch.equal(out, outs[0])
+
+
+def test_grouped_gemm_nan_stays_in_its_row():
+    K, N = 384, 256
+    x = torch.randn((70, K), generator=gen(2))
+    x[33, 200] = float("nan")
+    a_q, a_s = quantized_rows(x)
+    w_q, w_s = quantized_weights(torch.randn((1, N, K), generator=gen(3)))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    out = torch.zeros((70, N), dtype=torch.bfloat16, device="cuda")
+    M.moe_fp8_grouped_gemm(a_q, a_s, torch.zeros(1, **i32), torch.full((1,), 70, **i32), w_q,
+                           w_s, out, M.alloc_fp8_workspace())
+    nan = out.isnan().cpu()
+    assert nan[33].all() and nan.sum() == N
+
+
+def test_grouped_gemm_reports_a_bucket_outside_the_rows():
+    K, N, rows = 128, 256, 40
+    a_q, a_s = quantized_rows(torch.randn((rows, K), generator=gen(2)))
+    w_q, w_s = quantized_weights(torch.randn((4, N, K), generator=gen(3)))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    first, counts = [0, 30, -3, 10], [10, 11, 2, 20]
+    out = torch.full((rows, N), 3.25, dtype=torch.bfloat16, device="cuda")
+    ws = M.alloc_fp8_workspace()
+    M.moe_fp8_grouped_gemm(a_q, a_s, torch.tensor(first, **i32), torch.tensor(counts, **i32),
+                           w_q, w_s, out, ws)
+    with pytest.raises(M.MoEError) as e:
+        M.moe_check_device_error(ws)
+    assert e.value.status == 6 and "bucket" in str(e.value)
+    M.moe_check_device_error(ws)  # read once
+    check_product(out, a_q, a_s, w_q, w_s, [0, 0, 0, 10], [10, 0, 0, 20])
+
+
+# ------------------------------------------------------------------ FFN
+FFN = [  # counts, d, f
+    ([1], 16, 16),
+    ([1, 0, 1], 256, 128),
+    ([130, 1, 0, 64], 272, 400),
+    ([300], 1520, 720),
+    ([1] * 40, 384, 144),
+    ([33, 0, 257, 129], 640, 1008),
+    ([2, 3], 4096, 1024),
+]
+
+
+def make_ffn(counts, d, f, seed=0, rows=None):
+    g = gen(seed)
+    E = len(counts)
+    first, used = starts(counts)
+    rows = used if rows is None else rows
+    cfg = M.make_config(rows, d, f, E, 1)
+    x_q, x_s = quantized_rows(torch.randn((rows, d), generator=g).bfloat16())
+    experts = M.Fp8Experts.quantize(
+        *(torch.randn(s, generator=g).cuda() / s[2] ** 0.5
+          for s in ((E, f, d), (E, f, d), (E, d, f))))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    offs = torch.tensor(first + [used], **i32)
+    kept = torch.tensor(counts, **i32)
+    h_q = torch.full((rows, f), 0.5, device="cuda").to(E4M3)
+    h_s = torch.full((rows, O.blocks(f)), 7.0, device="cuda")
+    y = torch.full((rows, d), 3.25, dtype=torch.bfloat16, device="cuda")
+    return cfg, x_q, x_s, offs, kept, experts, h_q, h_s, y, first
+
+
+@pytest.mark.parametrize("counts,d,f", FFN)
+def test_ffn(counts, d, f):
+    cfg, x_q, x_s, offs, kept, experts, h_q, h_s, y, first = make_ffn(
+        counts, d, f, rows=sum(counts) + 3)
+    ws = M.alloc_fp8_workspace()
+    M.moe_expert_ffn_fp8(cfg, x_q, x_s, offs, kept, experts, h_q, h_s, y, ws)
+    M.moe_check_device_error(ws)
+    # the down product of the hidden rows that the kernel wrote
+    check_product(y, h_q, h_s, experts.w_down, experts.down_scale, first, counts)
+    # the hidden rows
+    x, h = O.rows_value(x_q, x_s), O.rows_value(h_q, h_s)
+    tol = O.sum_error(d)
+    for e, (r0, c) in enumerate(zip(first, counts)):
+        if c == 0:
+            continue
+        at = slice(r0, r0 + c)
+        gate, gm = O.product(x[at], O.weight_value(experts.w_gate[e], experts.gate_scale[e]))
+        up, um = O.product(x[at], O.weight_value(experts.w_up[e], experts.up_scale[e]))
+        act = gate * torch.sigmoid(gate)
+        ref = act * up
+        # |silu'| < 1.1; exp, the two additions, divisions and products of silu and of the
+        # quantisation: within 32 steps of fp32
+        room = tol * (1.1 * gm * up.abs() + um * act.abs()) + 1.1 * tol * tol * gm * um
+        room = room + 32 * 2.0 ** -24 * ref.abs()
+        # the block's scale is 1 / 448 of its largest magnitude: a quotient is off by half a
+        # step, at most 2^-4 of itself or 2^-10 in the smallest steps
+        pad = O.blocks(f) * O.BLOCK - f
+        big = torch.nn.functional.pad(ref.abs() + room, (0, pad)).unflatten(
+            1, (-1, O.BLOCK)).amax(2).repeat_interleave(O.BLOCK, 1)[:, :f]
+        step = torch.maximum(O.E4M3_HALF_STEP * (ref.abs() + room), 2.0 ** -10 * big / 448)
+        assert ((h[at] - ref).abs() <= (1 + 2.0 ** -20) * (step + room)).all(), e
+        s_ref = big[:, ::O.BLOCK] / 448
+        off = (h_s[at].cpu().double() - s_ref).abs()
+        rb = torch.nn.functional.pad(room, (0, pad)).unflatten(1, (-1, O.BLOCK)).amax(2)
+        assert (off <= 2 * rb / 448 + 2.0 ** -23 * s_ref).all(), e
+    for t, v in ((h_q.float(), 0.5), (h_s, 7.0)):
+        assert (t[sum(counts):] == v).all()
+
+
+def test_ffn_empty_hidden_row_is_zero():
+    """A zero row gives h = 0 (scale 2^-100 / 448) and y = 0; other rows are as without it."""
+    cfg, x_q, x_s, offs, kept, experts, h_q, h_s, y, _ = make_ffn([5, 4], 272, 144)
+    x_q.view(torch.uint8)[2] = 0
+    M.moe_expert_ffn_fp8(cfg, x_q, x_s, offs, kept, experts, h_q, h_s, y, M.alloc_fp8_workspace())
+    assert (h_q.float()[2] == 0).all() and (y[2] == 0).all()
+    assert (h_s[2].double() == np.float32(2.0 ** -100) / np.float32(448)).all()
+    assert torch.isfinite(y).all() and (y[1] != 0).any() and (y[3] != 0).any()
+
+
+def test_ffn_nan_row_stays_in_its_row():
+    cfg, x_q, x_s, offs, kept, experts, h_q, h_s, y, _ = make_ffn([40, 60], 272, 400)
+    x_q.view(torch.uint8)[41, 7] = 0x7F
+    M.moe_expert_ffn_fp8(cfg, x_q, x_s, offs, kept, experts, h_q, h_s, y, M.alloc_fp8_workspace())
+    nan = y.isnan().cpu()
+    assert nan[41].all() and nan.sum() == 272 and h_s[41].isnan().all()
+
+
+# ------------------------------------------------------------------ the layer
+LAYERS = [
+    W.reduced(W.MIXTRAL_8X7B, 300, 256, 384, capacity_factor=1.25),
+    W.reduced(W.DSV3_PREFILL_ZIPF, 600, 256, 128, capacity_factor=0.8, n_groups=8, topk_groups=4,
+              bias_mode=1, drop_policy=2),
+    W.reduced(W.MIXTRAL_8X22B_MIXED, 500, 272, 144, n_decode_tokens=8, layout=W.LAYOUT_PADDED),
+    W.reduced(W.MIXTRAL_8X7B, 1, 256, 128),
+]
+
+
+@pytest.mark.parametrize("shape", LAYERS, ids=lambda s: s.name)
+def test_layer(shape):
+    """The whole layer equals its stages called one by one, its routing and statistics equal
+    the bf16 layer's, and its products are right for the rows that dispatch kept."""
+    inp = W.make_inputs(shape, device="cuda")
+    cfg = M.config_from_shape(shape)
+    experts = M.Fp8Experts.quantize(inp.w_gate, inp.w_up, inp.w_down)
+    layer = M.MoELayerFp8(cfg, inp.w_router, experts, inp.logit_bias)
+    out = layer(inp.x).clone()
+    layer.check_device_error()
+    b, fb = layer.bufs, layer.fp8_bufs
+    # routing, dispatch and statistics as a bf16 layer's
+    ref = M.LayerBuffers.allocate(cfg)
+    ws = M.alloc_workspace(cfg)
+    M.moe_route(cfg, inp.x, inp.w_router, inp.logit_bias, ref.logits, ref.topk_idx, ref.topk_w, ws)
+    M.moe_dispatch_scored(cfg, inp.x, ref.topk_idx, ref.logits, inp.logit_bias,
+                          ref.routed_counts, ref.kept_counts, ref.expert_offsets, ref.assign_row,
+                          ref.token_of_row, None, ws)
+    for name in ("topk_idx", "topk_w", "routed_counts", "kept_counts", "expert_offsets",
+                 "assign_row"):
+        assert torch.equal(getattr(b, name), getattr(ref, name)), name
+    stats = M.stats_buffer()
+    assert M.moe_load_stats(cfg, ref.routed_counts, ref.kept_counts, ref.assign_row,
+                            stats) == b.stats_dict()
+    # the stages
+    s = M.Fp8LayerBuffers.allocate(cfg)
+    for t in (s.x_q, s.h_q):
+        t.view(torch.uint8).fill_(0x11)
+    s.layer.y_perm.fill_(3.25)
+    M.moe_fp8_permute_rows(cfg, inp.x, ref.assign_row, s.x_q, s.x_scale)
+    fws = M.alloc_fp8_workspace()
+    M.moe_expert_ffn_fp8(cfg, s.x_q, s.x_scale, ref.expert_offsets, ref.kept_counts, experts,
+                         s.h_q, s.h_scale, s.layer.y_perm, fws)
+    M.moe_combine(cfg, s.layer.y_perm, ref.assign_row, ref.topk_w, s.layer.out)
+    assert torch.equal(s.layer.out, out)
+    first = ref.expert_offsets[:-1].tolist()
+    counts = ref.kept_counts.tolist()
+    tq, _ = O.quantize_rows(inp.x.cpu())
+    token = ref.token_of_row.tolist()
+    for r0, c in zip(first, counts):
+        for r in range(r0, r0 + c):
+            assert np.array_equal(codes(s.x_q)[r], tq[token[r]])
+    check_product(s.layer.y_perm, s.h_q, s.h_scale, experts.w_down, experts.down_scale, first,
+                  counts)
+    assert torch.equal(layer(inp.x), out)
+
+
+def test_layer_is_near_the_bf16_layer():
+    """Six roundings to e4m3 meet in an output (x twice, gate, up, h, down): each off by at most
+    2^-4 of its entry, independent over hundreds of terms, so the outputs' norm is off by less
+    than sqrt(6) x 2^-4."""
+    shape = W.reduced(W.MIXTRAL_8X7B, 256, 512, 640)
+    inp = W.make_inputs(shape, device="cuda")
+    cfg = M.config_from_shape(shape)
+    a = M.MoELayer(cfg, inp.w_router, inp.w_gate, inp.w_up, inp.w_down, inp.logit_bias)(inp.x)
+    experts = M.Fp8Experts.quantize(inp.w_gate, inp.w_up, inp.w_down)
+    b = M.MoELayerFp8(cfg, inp.w_router, experts, inp.logit_bias)(inp.x)
+    off = (a.double() - b.double()).norm() / a.double().norm()
+    assert 0 < off < 6 ** 0.5 / 16
+
+
+def test_layer_captured_into_a_graph():
+    shape = W.reduced(W.DSV3_DECODE, 64, 256, 128)
+    inp = W.make_inputs(shape, device="cuda")
+    cfg = M.config_from_shape(shape)
+    experts = M.Fp8Experts.quantize(inp.w_gate, inp.w_up, inp.w_down)
+    layer = M.MoELayerFp8(cfg, inp.w_router, experts, inp.logit_bias)
+    x = inp.x.clone()
+    layer(x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=side):
+        layer(x, side)
+    other = M.MoELayerFp8(cfg, inp.w_router, experts, inp.logit_bias)
+    for seed in range(3):
+        new = W.make_inputs(shape.replace(seed=seed + 50), device="cuda", weights=False).x
+        x.copy_(new)
+        graph.replay()
+        got = layer.bufs.out.clone()
+        assert torch.equal(got, other(new))
+    layer.check_device_error()

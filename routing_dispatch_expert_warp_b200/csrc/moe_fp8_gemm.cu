@@ -67,17 +67,41 @@ struct Fp8Params {
   uint64_t wait_ns;
 };
 
-// One fp32 accumulator row of a thread as packed pairs: acc += v * s for 32 columns.
-__device__ __forceinline__ void fma_chunk(uint64_t (&acc)[64], int at, const uint32_t (&v)[32],
-                                          float s) {
-  uint64_t ss;
-  asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "r"(__float_as_uint(s)));
+// acc += v * s for 16 columns of a thread's accumulator row, as packed pairs of fp32 FMAs.
+__device__ __forceinline__ void fma_chunk(uint64_t (&acc)[64], int at, const uint32_t (&v)[16],
+                                          uint64_t ss) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < 8; ++i) {
     uint64_t vv;
     asm("mov.b64 %0, {%1, %2};" : "=l"(vv) : "r"(v[2 * i]), "r"(v[2 * i + 1]));
     asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[at + i]) : "l"(vv), "l"(ss));
   }
+}
+
+__device__ __forceinline__ uint64_t both(float s) {
+  uint64_t ss;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "r"(__float_as_uint(s)));
+  return ss;
+}
+
+// 32 lanes x 16 columns of tensor memory; the wait makes the loaded values usable.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
 }
 
 __device__ __forceinline__ float2 unpack2(uint64_t v) {
@@ -364,15 +388,21 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
           break;
         }
         if (live) {
+          // 16 columns at a time, the next ones on their way while these are summed
           tc_fence_after();
           const uint32_t ta = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                               static_cast<uint32_t>(acc_i * ACC_COLS) + col0;
+          const uint64_t ss0 = both(f0), ss1 = both(f1);
+          uint32_t v[2][16];
+          tmem_ld16(ta, v[0]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32];
-            tmem_ld32(ta + (GATED ? (c & 1) * 32 + (c >> 1) * 128 : c * 32), v);
-            tmem_ld_wait();
-            fma_chunk(acc, c * 16, v, GATED && c >= 2 ? f1 : f0);
+          for (int c = 0; c < 8; ++c) {
+            tmem_wait16(v[c & 1]);
+            if (c < 7) {
+              const int n = c + 1;
+              tmem_ld16(ta + (GATED ? (n & 3) * 16 + (n >> 2) * 128 : n * 16), v[n & 1]);
+            }
+            fma_chunk(acc, c * 8, v[c & 1], GATED && c >= 4 ? ss1 : ss0);
           }
           tc_fence_before();
         }

@@ -8,22 +8,33 @@
 // warps, which take the tensor cores' partial tile out of tensor memory after each block while
 // the next block's MMAs fill the other half of it.
 //
-// Tile: 128 bucket rows x 256 weight rows.  FP8_LINEAR: 256 output columns.  FP8_GATED: 128
-// columns of h, the weight rows being 128 of W_gate over the same 128 of W_up, so gate and up
-// of an entry meet in one thread and a tile's 128 columns are one block of h's quantisation:
-// the epilogue writes h = silu(gate) * up as e4m3 with its scale, and no h in higher precision
-// exists.
+// Tile: 128 bucket rows x 256 weight rows, as two halves of 128 weight rows that share the rows'
+// tile in shared memory and have accumulators, barriers and epilogue warps of their own.
+// FP8_LINEAR: half h is output columns [128 h, +128) of the tile's 256.  FP8_GATED: the tile is
+// 128 columns of h, half h 64 of them: 64 rows of W_gate over the same 64 of W_up, so gate and
+// up of an entry meet in one thread, and the tile's 128 columns are one block of h's
+// quantisation: the epilogue writes h = silu(gate) * up as e4m3 with its scale, and no h in
+// higher precision exists.
 //
-// Block = 10 warps, one block per SM, persistent over tiles (numbered expert by expert,
+// Block = 12 warps, one block per SM, persistent over tiles (numbered expert by expert,
 // column block by column block, row blocks innermost, so that blocks running at the same time
-// share weight tiles through L2; the table of tiles is built on the device):
-//   warp 0 (one lane)  TMA producer: 128 x 128 bytes of rows, 256 x 128 of weights, 128-byte
-//                      swizzle, 4 stages.  Of a bucket's last rows only as many groups of 32
-//                      as hold rows are loaded.
-//   warp 1 (one lane)  4 MMAs (K = 32 each) a stage into one of two accumulators (256 columns).
-//   warps 2-9          epilogue: warp w has lane quarter w % 4 of tensor memory and half
-//                      (w - 2) / 4 of the accumulator's columns: each thread sums 128 entries
-//                      of one row.  A warp without bucket rows only keeps step.
+// share weight tiles through L2; the table of tiles is built on the device).  Every tile starts
+// at stage 0 of the ring of 4 and at accumulator 0; each barrier's parity is a bit of a mask.  (The loops over the
+// reduction are not unrolled: four copies of the epilogue's missed the instruction cache.)
+//   warp 0             TMA producer: 128 x 128 bytes of rows, 256 x 128 of weights, 128-byte
+//                      swizzle.  Of a bucket's last rows only as many groups of 32 as hold rows
+//                      are loaded.
+//   warps 1, 2         MMA issuers, one for each half: 4 MMAs (128 x 128 x 32) a block into one
+//                      of the half's two accumulators; one commit tells the producer that the
+//                      half has left the stage and the epilogue that its sums are there.
+//   warp 3             scales: the products a_scale * w_scale of 4 blocks at a time, a turn
+//                      ahead, from global to shared memory.
+//   warps 4-11         epilogue: warp w has lane quarter w % 4 of tensor memory in half
+//                      (w - 4) / 4: each thread sums 128 entries of one row.  A warp without
+//                      bucket rows only keeps step.
+// A hand-over between an MMA issuer and an epilogue takes some 200 cycles each way.  With the
+// halves apart, four accumulators of 128 columns are on their way round instead of two of 256,
+// and one half's epilogue computes while the other's waits.
 // Every wait is bounded as in the bf16 expert GEMM.
 #include <cuda_fp8.h>
 
@@ -35,15 +46,23 @@ namespace {
 constexpr int BM = 128;
 constexpr int BK = 128;  // bytes = e4m3 values of a stage's rows: one block of the scales
 constexpr int BN = 256;
+constexpr int HALF_N = BN / 2;
 constexpr int STAGES = 4;
 constexpr int A_BYTES = BM * BK;
 constexpr int B_BYTES = BN * BK;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int CTRL_WARPS = 4;
 constexpr int EPI_WARPS = 8;
-constexpr int THREADS = 64 + 32 * EPI_WARPS;
-constexpr int ACC_COLS = 256;
-constexpr int TMEM_COLS = 512;
-constexpr int DYN_SMEM = STAGES * STAGE_BYTES + 1024;
+constexpr int THREADS = 32 * (CTRL_WARPS + EPI_WARPS);
+// The launch's 168 registers a thread are split anew: 128 x 72 + 256 x 216 = 384 x 168.  (The
+// split stands at the head of each role's branch: the compiler goes by it there.)
+constexpr int LAUNCH_REGS = 168, CTRL_REGS = 72, EPI_REGS = 216;
+static_assert(32 * (CTRL_WARPS * CTRL_REGS + EPI_WARPS * EPI_REGS) <= THREADS * LAUNCH_REGS,
+              "setmaxnreg.inc would wait for registers that the block does not have");
+constexpr int TMEM_COLS = 512;  // 2 halves x 2 accumulators x 128
+// per epilogue warp: 32 rows x 64 bytes of output on their way to whole-row stores
+constexpr int OUT_STAGE = 32 * 64;
+constexpr int DYN_SMEM = STAGES * STAGE_BYTES + EPI_WARPS * OUT_STAGE + 1024;  // + alignment
 
 enum Mode { FP8_LINEAR = 0, FP8_GATED = 1 };
 
@@ -68,23 +87,20 @@ struct Fp8Params {
 };
 
 // acc += v * s for 16 columns of a thread's accumulator row, as packed pairs of fp32 FMAs.
-__device__ __forceinline__ void fma_chunk(uint64_t (&acc)[64], int at, const uint32_t (&v)[16],
-                                          uint64_t ss) {
+__device__ __forceinline__ void fma16(float2 (&acc)[64], int at, const uint32_t (&v)[16],
+                                      float s) {
+  const float2 ss = make_float2(s, s);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    uint64_t vv;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(vv) : "r"(v[2 * i]), "r"(v[2 * i + 1]));
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[at + i]) : "l"(vv), "l"(ss));
-  }
+  for (int i = 0; i < 8; ++i)
+    acc[at / 2 + i] = __ffma2_rn(
+        make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), ss,
+        acc[at / 2 + i]);
+}
+__device__ __forceinline__ float get(const float2 (&acc)[64], int i) {
+  return i & 1 ? acc[i / 2].y : acc[i / 2].x;
 }
 
-__device__ __forceinline__ uint64_t both(float s) {
-  uint64_t ss;
-  asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "r"(__float_as_uint(s)));
-  return ss;
-}
-
-// 32 lanes x 16 columns of tensor memory; the wait makes the loaded values usable.
+// 32 lanes x 16 columns of tensor memory, on their way until tmem_ld_wait().
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -104,10 +120,40 @@ __device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
                : "memory");
 }
 
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-  uint32_t lo, hi;
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
-  return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+// One arrival by the threads whose `who` is not 0, without a branch.
+__device__ __forceinline__ void arrive_if(uint64_t* bar, uint32_t who) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_addr(bar)),
+      "r"(who)
+      : "memory");
+}
+
+// 4 scales from block kb on (0 past the last of n).
+__device__ __forceinline__ float4 scales4(const float* s, int kb, int n) {
+  if ((n & 3) == 0)
+    return kb < n ? __ldg(reinterpret_cast<const float4*>(s + kb)) : make_float4(0.f, 0.f, 0.f, 0.f);
+  return make_float4(kb < n ? __ldg(s + kb) : 0.f, kb + 1 < n ? __ldg(s + kb + 1) : 0.f,
+                     kb + 2 < n ? __ldg(s + kb + 2) : 0.f, kb + 3 < n ? __ldg(s + kb + 3) : 0.f);
+}
+__device__ __forceinline__ float pick(const float4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+template <int REGS>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
 }
 
 __device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
@@ -128,7 +174,7 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
 }
 
 __device__ __forceinline__ float silu_mul(float g, float u) {
-  return g / (1.0f + __expf(-g)) * u;
+  return __fdividef(g, 1.0f + __expf(-g)) * u;
 }
 
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
@@ -196,6 +242,29 @@ __device__ __forceinline__ Tile decode(const Buckets& t, const Fp8Params& p, int
   return r;
 }
 
+// 64 bytes of each of a warp's 32 rows, a row's 16 words in its lane: through `buf` (16-byte
+// piece c of row r at r * 64 + ((c ^ ((r >> 1) & 3)) * 16)), so that 4 lanes store a row's 64
+// bytes at once, 8 rows an instruction.  Only rows before `rows` and the first `bytes` of the 64
+// (a multiple of 16) are stored; to: the first row's 64 bytes, rows `stride` bytes apart.
+__device__ __forceinline__ void store_rows64(uint8_t* buf, const uint32_t (&w)[16], uint8_t* to,
+                                             int64_t stride, int rows, int bytes, int lane) {
+  const int sw = (lane >> 1) & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<uint4*>(buf + lane * 64 + ((i ^ sw) << 4)) =
+        make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  __syncwarp();
+  const int seg = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2);
+    if (r < rows && seg * 16 < bytes)
+      *reinterpret_cast<uint4*>(to + r * stride + seg * 16) =
+          *reinterpret_cast<const uint4*>(buf + r * 64 + ((seg ^ ((r >> 1) & 3)) << 4));
+  }
+  __syncwarp();
+}
+
 // tm_a: rows in boxes of 128, tm_a32: the same rows in boxes of 32; tm_b0, tm_b1: the weights.
 template <int MODE>
 __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
@@ -205,15 +274,17 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
   constexpr bool GATED = MODE == FP8_GATED;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[STAGES];
-  __shared__ __align__(8) uint64_t empty_bar[STAGES];
-  __shared__ __align__(8) uint64_t tfull_bar[2];
-  __shared__ __align__(8) uint64_t tempty_bar[2];
+  __shared__ __align__(8) uint64_t done_bar[2][STAGES];  // a half's MMAs on the stage are done
+  __shared__ __align__(8) uint64_t tempty_bar[2][2];     // [half][accumulator]
+  __shared__ __align__(8) uint64_t sfull_bar[2];         // 4 blocks' scales are there
+  __shared__ __align__(8) uint64_t sfree_bar[2];         // ... and have been read
   __shared__ __align__(8) uint64_t amax_bar;
-  __shared__ __align__(8) uint64_t drain_bar;
+  __shared__ __align__(8) uint64_t drain_bar[2];
   __shared__ uint32_t tmem_base_s;
   __shared__ volatile int abort_s;
   __shared__ Buckets bk;
-  __shared__ uint32_t amax_s[2][2][BM];  // GATED: [tile parity][column half][row]
+  __shared__ float scale_s[2][4][2][BM];  // [turn][block][LINEAR: half, GATED: gate, up][row]
+  __shared__ uint32_t amax_s[2][2][BM];   // GATED: [tile parity][column half][row]
 
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -234,14 +305,16 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
   } else if (threadIdx.x == 64) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full_bar[s], 1);
-      mbar_init(&empty_bar[s], 1);
+      mbar_init(&done_bar[0][s], 1);
+      mbar_init(&done_bar[1][s], 1);
     }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(&tfull_bar[a], 1);
-      mbar_init(&tempty_bar[a], EPI_WARPS);
+    for (int i = 0; i < 4; ++i) mbar_init(&tempty_bar[i >> 1][i & 1], EPI_WARPS / 2);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sfull_bar[i], 1);
+      mbar_init(&sfree_bar[i], EPI_WARPS);
+      mbar_init(&drain_bar[i], 1);
     }
     mbar_init(&amax_bar, EPI_WARPS);
-    mbar_init(&drain_bar, 1);
     abort_s = 0;
     fence_barrier_init();
   }
@@ -251,167 +324,211 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
 
   const uint32_t tmem_base = tmem_base_s;
   const int total = bk.tile_base[p.E];
+  const int KB = p.kb;
+
+  // The whole warp waits for a barrier.  Once a wait has run out, here or elsewhere in the
+  // block, every role's next wait fails and the roles unwind.
+  auto await = [&](uint64_t* bar, uint32_t parity, unsigned site, int tile) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const bool got = mbar_wait(bar, parity, p.wait_ns, &abort_s);
+    if (__all_sync(0xffffffffu, got)) return true;
+    if (lane == 0) {
+      if (!abort_s)
+        record_error(p.status, DEV_TIMEOUT, site, static_cast<unsigned long long>(tile));
+      abort_s = 1;
+    }
+    return false;
+  };
 
   if (warp == 0) {
     // ---------------------------------------------------------------- TMA producer
-    if (lane == 0) {
-      int s = 0;
-      uint32_t ph = 0;
-      uint32_t armed = 0, armed_parity = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-        const Tile t = decode(bk, p, tile);
-        const int groups = t.valid > 96 ? 4 : (t.valid + 31) >> 5;  // of 32 rows
-        for (int kb = 0; kb < p.kb; ++kb) {
-          if (!mbar_wait(&empty_bar[s], ph ^ 1u, p.wait_ns, &abort_s)) {
-            if (!abort_s)
-              record_error(p.status, DEV_TIMEOUT, 41, static_cast<unsigned long long>(tile));
-            abort_s = 1;
+    regs_dec<CTRL_REGS>();
+    uint32_t fills = 0;  // bit s: parity of stage s's next fill
+    uint32_t armed = 0, armed_parity = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+      const Tile t = decode(bk, p, tile);
+      const int groups = t.valid > BM - 32 ? BM / 32 : (t.valid + 31) >> 5;  // of 32 rows
+#pragma unroll 1
+      for (int kb = 0; kb < KB; ++kb) {
+          const int s = kb & (STAGES - 1);
+          const uint32_t par = (fills >> s) & 1u;
+          if (!await(&done_bar[0][s], par ^ 1u, 41, tile) ||
+              !await(&done_bar[1][s], par ^ 1u, 41, tile)) {
             ok = false;
             break;
           }
           uint8_t* sa = smem + s * STAGE_BYTES;
           uint8_t* sb = sa + A_BYTES;
-          mbar_arrive_expect_tx(&full_bar[s], B_BYTES + groups * 32 * BK);
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&full_bar[s], B_BYTES + groups * 32 * BK);
+            if (GATED) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint8_t* to = sb + h * HALF_N * BK;
+                tma_load_3d(to, &tm_b0, &full_bar[s], kb * BK, t.nb * 128 + h * 64, t.e);
+                tma_load_3d(to + 64 * BK, &tm_b1, &full_bar[s], kb * BK, t.nb * 128 + h * 64, t.e);
+              }
+            } else {
+              tma_load_3d(sb, &tm_b0, &full_bar[s], kb * BK, t.nb * BN, t.e);
+            }
+            if (groups == 4) {
+              tma_load_2d(sa, &tm_a, &full_bar[s], kb * BK, t.row0);
+            } else {
+              for (int g = 0; g < groups; ++g)
+                tma_load_2d(sa + g * 32 * BK, &tm_a32, &full_bar[s], kb * BK, t.row0 + g * 32);
+            }
+          }
+          __syncwarp();
           armed |= 1u << s;
-          armed_parity = (armed_parity & ~(1u << s)) | (ph << s);
-          if (groups == 4) {
-            tma_load_2d(sa, &tm_a, &full_bar[s], kb * BK, t.row0);
-          } else {
-            for (int g = 0; g < groups; ++g)
-              tma_load_2d(sa + g * 32 * BK, &tm_a32, &full_bar[s], kb * BK, t.row0 + g * 32);
-          }
-          if (GATED) {
-            tma_load_3d(sb, &tm_b0, &full_bar[s], kb * BK, t.nb * 128, t.e);
-            tma_load_3d(sb + B_BYTES / 2, &tm_b1, &full_bar[s], kb * BK, t.nb * 128, t.e);
-          } else {
-            tma_load_3d(sb, &tm_b0, &full_bar[s], kb * BK, t.nb * BN, t.e);
-          }
-          if (++s == STAGES) {
-            s = 0;
-            ph ^= 1u;
-          }
-        }
+          armed_parity = (armed_parity & ~(1u << s)) | (par << s);
+          fills ^= 1u << s;
       }
-      // every fill this thread armed must land before the block can exit
-      for (int q = 0; q < STAGES; ++q)
-        if ((armed >> q) & 1u)
-          mbar_wait(&full_bar[q], (armed_parity >> q) & 1u, p.wait_ns, nullptr);
     }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_e4m3_f32(BM, BN);
-      int s = 0;
-      uint32_t ph = 0;
-      int acc = 0;
-      uint32_t aph = 0;
-      bool ok = true, issued = false;
-      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-        for (int kb = 0; kb < p.kb; ++kb) {
-          if (!mbar_wait(&tempty_bar[acc], aph ^ 1u, p.wait_ns, &abort_s) ||
-              !mbar_wait(&full_bar[s], ph, p.wait_ns, &abort_s)) {
-            if (!abort_s)
-              record_error(p.status, DEV_TIMEOUT, 42, static_cast<unsigned long long>(tile));
-            abort_s = 1;
+    // every fill must land before the block can exit
+    for (int s = 0; s < STAGES; ++s)
+      if ((armed >> s) & 1u)
+        mbar_wait(&full_bar[s], (armed_parity >> s) & 1u, p.wait_ns, nullptr);
+    __syncwarp();
+  } else if (warp < 3) {
+    // ---------------------------------------------------------------- MMA issuers
+    regs_dec<CTRL_REGS>();
+    constexpr uint32_t idesc = idesc_e4m3_f32(BM, HALF_N);
+    const int h = warp - 1;
+    const uint64_t a_desc = sw128_kmajor_desc(smem_addr(smem));
+    const uint64_t b_desc = sw128_kmajor_desc(smem_addr(smem) + A_BYTES + h * HALF_N * BK);
+    uint32_t fills = 0, uses = 0;  // parities: stage s's next fill, accumulator j's next use
+    bool ok = true, issued = false;
+    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+#pragma unroll 1
+      for (int kb = 0; kb < KB; ++kb) {
+          const int s = kb & (STAGES - 1), j = kb & 1;
+          if (!await(&full_bar[s], (fills >> s) & 1u, 42, tile) ||
+              !await(&tempty_bar[h][j], ((uses >> j) & 1u) ^ 1u, 42, tile)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a_addr = smem_addr(smem + s * STAGE_BYTES);
-          const uint32_t b_addr = a_addr + A_BYTES;
-          const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * ACC_COLS);
+          if (elect_one()) {
+            const uint32_t d_tmem = tmem_base + static_cast<uint32_t>((2 * h + j) * HALF_N);
 #pragma unroll
-          for (int kk = 0; kk < BK / 32; ++kk)
-            tc_mma_e4m3(d_tmem, sw128_kmajor_desc(a_addr + kk * 32),
-                        sw128_kmajor_desc(b_addr + kk * 32), idesc, kk != 0 ? 1u : 0u);
-          issued = true;
-          tc_commit(&empty_bar[s]);
-          tc_commit(&tfull_bar[acc]);
-          if (++s == STAGES) {
-            s = 0;
-            ph ^= 1u;
+            for (int kk = 0; kk < BK / 32; ++kk)  // descriptors count 16-byte units
+              tc_mma_e4m3(d_tmem, a_desc + (s * STAGE_BYTES + kk * 32) / 16,
+                          b_desc + (s * STAGE_BYTES + kk * 32) / 16, idesc, kk != 0 ? 1u : 0u);
+            tc_commit(&done_bar[h][s]);
           }
-          acc ^= 1;
-          if (acc == 0) aph ^= 1u;
-        }
+          __syncwarp();
+          issued = true;
+          fills ^= 1u << s;
+          uses ^= 1u << j;
       }
-      if (!ok && issued) {  // MMAs still reading smem / writing TMEM must finish first
-        tc_commit(&drain_bar);
-        mbar_wait(&drain_bar, 0, p.wait_ns, nullptr);
+    }
+    if (!ok && issued) {  // MMAs still reading smem / writing TMEM must finish first
+      if (elect_one()) tc_commit(&drain_bar[h]);
+      mbar_wait(&drain_bar[h], 0, p.wait_ns, nullptr);
+      __syncwarp();
+    }
+  } else if (warp == 3) {
+    // ---------------------------------------------------------------- scales
+    regs_dec<CTRL_REGS>();
+    // A lane has rows lane + 32 i of the tile.  (The epilogue's threads loading their own rows'
+    // scales took a fifth of its time: 32 rows' lanes are 32 passes of the L1.)
+    uint32_t turns = 0;  // of 4 blocks, over all tiles
+    bool ok = true;
+    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+      const Tile t = decode(bk, p, tile);
+      const float* sa = p.a_scale + (static_cast<int64_t>(t.row0) + lane) * KB;
+      const int64_t w_row = static_cast<int64_t>(t.e) * p.nsb;
+      // LINEAR: the two halves' blocks of columns (one past the last is never stored)
+      const float* s0 = p.w_scale0 + (w_row + (GATED ? t.nb : 2 * t.nb)) * KB;
+      const float* s1 = GATED ? p.w_scale1 + (w_row + t.nb) * KB
+                              : p.w_scale0 + (w_row + min(2 * t.nb + 1, p.nsb - 1)) * KB;
+      for (int k0 = 0; k0 < KB; k0 += 4) {
+        float4 a[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          a[i] = lane + 32 * i < t.valid
+                     ? scales4(sa + static_cast<int64_t>(32 * i) * KB, k0, KB)
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 w0 = scales4(s0, k0, KB), w1 = scales4(s1, k0, KB);
+        const uint32_t b = turns & 1u;
+        if (!await(&sfree_bar[b], ((turns >> 1) & 1u) ^ 1u, 45, tile)) {
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            scale_s[b][k][0][lane + 32 * i] = pick(a[i], k) * pick(w0, k);
+            scale_s[b][k][1][lane + 32 * i] = pick(a[i], k) * pick(w1, k);
+          }
+        __syncwarp();
+        arrive_if(&sfull_bar[b], lane == 0);
+        ++turns;
       }
     }
   } else {
     // ---------------------------------------------------------------- epilogue
-    const int q = warp & 3;           // TMEM lane quarter this warp may access
-    const int half = (warp - 2) >> 2; // its half of the accumulator's columns
-    const int r = q * 32 + lane;      // accumulator row of this thread
-    // GATED: gate columns [64 half, +64) and the up columns 128 further; else [128 half, +128)
-    const uint32_t col0 = static_cast<uint32_t>(GATED ? 64 * half : 128 * half);
-    int acc_i = 0;
-    uint32_t aph = 0;
-    uint32_t xph = 0;
+    regs_inc<EPI_REGS>();
+    const int q = warp & 3;                     // TMEM lane quarter this warp may access
+    const int half = (warp - CTRL_WARPS) >> 2;  // which half's accumulators
+    const int r = q * 32 + lane;                // accumulator row of this thread
+    const uint32_t first = lane == 0;
+    const uint32_t ta = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                        static_cast<uint32_t>(2 * half * HALF_N);
+    uint8_t* stage_out = smem + STAGES * STAGE_BYTES + (warp - CTRL_WARPS) * OUT_STAGE;
+    uint32_t fills = 0;  // bit s: parity of stage s's next fill
+    uint32_t turns = 0, xph = 0;
     bool ok = true;
     for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
       const Tile t = decode(bk, p, tile);
       const bool live = 32 * q < t.valid;  // the warp has bucket rows
-      const bool row_ok = r < t.valid;
-      const int64_t row = static_cast<int64_t>(t.row0) + (row_ok ? r : 0);
-      const float* sa = p.a_scale + row * p.kb;
-      // the weight's block of columns; one past the last is summed but never stored
-      const int sb = GATED ? t.nb : min(2 * t.nb + half, p.nsb - 1);
-      const int64_t sw = (static_cast<int64_t>(t.e) * p.nsb + sb) * p.kb;
-      const float* s0 = p.w_scale0 + sw;
-      const float* s1 = GATED ? p.w_scale1 + sw : nullptr;
-      uint64_t acc[64];
+      float2 acc[64];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0ull;
-      float na = 0.f, n0 = 0.f, n1 = 0.f;  // the next block's scales
-      if (live) {
-        na = __ldg(sa);
-        n0 = __ldg(s0);
-        if (GATED) n1 = __ldg(s1);
-      }
-      for (int kb = 0; kb < p.kb; ++kb) {
-        const float f0 = na * n0, f1 = GATED ? na * n1 : 0.f;
-        if (live && kb + 1 < p.kb) {
-          na = __ldg(sa + kb + 1);
-          n0 = __ldg(s0 + kb + 1);
-          if (GATED) n1 = __ldg(s1 + kb + 1);
-        }
-        const bool got = mbar_wait(&tfull_bar[acc_i], aph, p.wait_ns, &abort_s);
-        if (!__all_sync(0xffffffffu, got)) {
-          if (lane == 0 && !abort_s)
-            record_error(p.status, DEV_TIMEOUT, 43, static_cast<unsigned long long>(tile));
-          abort_s = 1;
+      for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
+#pragma unroll 1
+      for (int kb = 0; kb < KB; ++kb) {
+        const int s = kb & (STAGES - 1), j = kb & 1;
+        const uint32_t b = turns & 1u;
+        if (s == 0 && !await(&sfull_bar[b], (turns >> 1) & 1u, 46, tile)) {
           ok = false;
           break;
         }
-        if (live) {
-          // 16 columns at a time, the next ones on their way while these are summed
-          tc_fence_after();
-          const uint32_t ta = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
-                              static_cast<uint32_t>(acc_i * ACC_COLS) + col0;
-          const uint64_t ss0 = both(f0), ss1 = both(f1);
-          uint32_t v[2][16];
-          tmem_ld16(ta, v[0]);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            tmem_wait16(v[c & 1]);
-            if (c < 7) {
-              const int n = c + 1;
-              tmem_ld16(ta + (GATED ? (n & 3) * 16 + (n >> 2) * 128 : n * 16), v[n & 1]);
-            }
-            fma_chunk(acc, c * 8, v[c & 1], GATED && c >= 4 ? ss1 : ss0);
-          }
-          tc_fence_before();
+        const float f = scale_s[b][s][GATED ? 0 : half][r];
+        const float g = GATED ? scale_s[b][s][1][r] : f;
+        if (!await(&done_bar[half][s], (fills >> s) & 1u, 43, tile)) {
+          ok = false;
+          break;
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&tempty_bar[acc_i]);
-        acc_i ^= 1;
-        if (acc_i == 0) aph ^= 1u;
+        fills ^= 1u << s;
+        if (live) {
+          tc_fence_after();
+          const uint32_t from = ta + static_cast<uint32_t>(j * HALF_N);
+          uint32_t v[2][16];
+          // 16 columns at a time, the next ones on their way while these are summed
+          tmem_ld16(from, v[0]);
+#pragma unroll
+          for (int c = 0; c < 7; ++c) {
+            tmem_wait16(v[c & 1]);
+            tmem_ld16(from + (c + 1) * 16, v[(c + 1) & 1]);
+            fma16(acc, 16 * c, v[c & 1], c >= 4 ? g : f);
+          }
+          tmem_wait16(v[1]);
+          tc_fence_before();
+          arrive_if(&tempty_bar[half][j], first);
+          fma16(acc, 16 * 7, v[1], g);
+        } else {
+          arrive_if(&tempty_bar[half][j], first);
+        }
+        if (s == STAGES - 1 || kb == KB - 1) {  // every lane has read the 4 blocks' scales
+          __syncwarp();
+          arrive_if(&sfree_bar[b], first);
+          ++turns;
+        }
       }
       if (!ok) break;
+      const int left = t.valid - 32 * q;  // rows of this warp, from its first
       if (GATED) {
         // h of this thread's 64 columns over its gate half of the accumulators, the row's
         // largest magnitude over both halves, then e4m3 and the scale
@@ -419,59 +536,50 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
         if (live) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const float2 g = unpack2(acc[i]), u = unpack2(acc[32 + i]);
-            const uint32_t h0 = __float_as_uint(silu_mul(g.x, u.x));
-            const uint32_t h1 = __float_as_uint(silu_mul(g.y, u.y));
-            m = max(m, max(h0 & 0x7FFFFFFFu, h1 & 0x7FFFFFFFu));
-            asm("mov.b64 %0, {%1, %2};" : "=l"(acc[i]) : "r"(h0), "r"(h1));
+            acc[i].x = silu_mul(acc[i].x, acc[32 + i].x);
+            acc[i].y = silu_mul(acc[i].y, acc[32 + i].y);
+            m = max(m, max(__float_as_uint(acc[i].x) & 0x7FFFFFFFu,
+                           __float_as_uint(acc[i].y) & 0x7FFFFFFFu));
+            if (i % 4 == 3) asm volatile("" ::: "memory");  // (not all quotients at once)
           }
         }
         amax_s[xph][half][r] = m;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&amax_bar);
-        const bool got = mbar_wait(&amax_bar, xph, p.wait_ns, &abort_s);
-        if (!__all_sync(0xffffffffu, got)) {
-          if (lane == 0 && !abort_s)
-            record_error(p.status, DEV_TIMEOUT, 44, static_cast<unsigned long long>(tile));
-          abort_s = 1;
-          break;
-        }
+        arrive_if(&amax_bar, first);
+        if (!await(&amax_bar, xph, 44, tile)) break;
         m = max(m, amax_s[xph][half ^ 1][r]);
         xph ^= 1u;
-        if (row_ok) {
+        if (live) {
           const bool bad = m >= 0x7F800000u;
           const float mf = fmaxf(__uint_as_float(m), 7.8886090522101181e-31f);  // 2^-100
           const float rs = __fdiv_rn(448.0f, mf);
-          const int col = t.nb * 128 + 64 * half;
-          uint8_t* to = p.h + row * p.N + col;
+          uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 a = unpack2(acc[8 * i + 2 * j]), b = unpack2(acc[8 * i + 2 * j + 1]);
-              w[j] = bad ? 0x7F7F7F7Fu : e4m3x4(a.x * rs, a.y * rs, b.x * rs, b.y * rs);
-            }
-            if (col + 16 * i < p.N)
-              *reinterpret_cast<uint4*>(to + 16 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int i = 0; i < 16; ++i) {
+            w[i] = e4m3x4(acc[2 * i].x * rs, acc[2 * i].y * rs, acc[2 * i + 1].x * rs,
+                          acc[2 * i + 1].y * rs);
+            if (bad) w[i] = 0x7F7F7F7Fu;
           }
-          if (half == 0)
-            p.h_scale[row * p.nsb + t.nb] =
+          const int col = t.nb * 128 + 64 * half;
+          store_rows64(stage_out, w, p.h + (static_cast<int64_t>(t.row0) + 32 * q) * p.N + col,
+                       p.N, left, p.N - col, lane);
+          if (half == 0 && lane < left)
+            p.h_scale[(static_cast<int64_t>(t.row0) + r) * p.nsb + t.nb] =
                 bad ? __uint_as_float(0x7FFFFFFFu) : __fdiv_rn(mf, 448.0f);
         }
-      } else if (row_ok) {
-        const int col = t.nb * BN + 128 * half;
-        __nv_bfloat16* to = p.out + row * p.N + col;
+      } else if (live) {
+        const int col = t.nb * BN + HALF_N * half;
+        uint8_t* to = reinterpret_cast<uint8_t*>(
+            p.out + (static_cast<int64_t>(t.row0) + 32 * q) * p.N + col);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          uint32_t w[4];
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[16];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 v = unpack2(acc[4 * i + j]);
-            w[j] = pack_bf16x2(v.x, v.y);
+          for (int i = 0; i < 16; ++i) {
+            w[i] = pack_bf16x2(get(acc, 32 * c + 2 * i), get(acc, 32 * c + 2 * i + 1));
           }
-          if (col + 8 * i < p.N)
-            *reinterpret_cast<uint4*>(to + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+          store_rows64(stage_out, w, to + 64 * c, static_cast<int64_t>(p.N) * 2, left,
+                       2 * (p.N - col - 32 * c), lane);
         }
       }
     }
@@ -520,10 +628,9 @@ cudaError_t launch(const CUtensorMap& a, const CUtensorMap& a32, const CUtensorM
   cudaError_t err = cudaFuncSetAttribute(fp8_grouped_gemm_kernel<MODE>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, DYN_SMEM);
   if (err != cudaSuccess) return err;
-  // at most one row block per bucket for its ragged end, and the rest full
+  // at most one ragged row block per bucket, the rest full
   int64_t tiles = (p.rows / BM + (p.rows < p.E ? p.rows : p.E)) * p.n_blocks;
   if (tiles > sm_count()) tiles = sm_count();
-  if (tiles < 1) tiles = 1;
   fp8_grouped_gemm_kernel<MODE><<<static_cast<unsigned>(tiles), THREADS, DYN_SMEM, st>>>(
       a, a32, b0, b1, p);
   note_launch();
@@ -544,8 +651,8 @@ cudaError_t launch_fp8_gemm(const Fp8Gemm& g, void* ws, uint64_t wait_ns, cudaSt
   const bool gated = g.w1 != nullptr;
   CUtensorMap a, a32, b0, b1;
   if (!map_rows(&a, g.a, g.rows, g.K, BM) || !map_rows(&a32, g.a, g.rows, g.K, 32) ||
-      !map_weights(&b0, g.w0, g.E, g.N, g.K, gated ? 128 : BN) ||
-      (gated && !map_weights(&b1, g.w1, g.E, g.N, g.K, 128))) {
+      !map_weights(&b0, g.w0, g.E, g.N, g.K, gated ? 64 : BN) ||
+      (gated && !map_weights(&b1, g.w1, g.E, g.N, g.K, 64))) {
     *why = "tensor map encoding failed (pointer alignment or sizes)";
     return cudaErrorInvalidValue;
   }

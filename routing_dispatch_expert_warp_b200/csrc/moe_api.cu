@@ -1108,6 +1108,7 @@ moe_status_t moe_expert_ffn_fp8(const moe_config_t* cfg, const void* x_q, const 
   g.h = nullptr;
   g.h_scale = nullptr;
   g.out = y_perm;
+  g.follows = true;
   return run_fp8_gemm(name, g, ws, stream);
 }
 

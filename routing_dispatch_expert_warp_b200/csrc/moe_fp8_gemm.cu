@@ -35,6 +35,12 @@
 // A hand-over between an MMA issuer and an epilogue takes some 200 cycles each way.  With the
 // halves apart, four accumulators of 128 columns are on their way round instead of two of 256,
 // and one half's epilogue computes while the other's waits.
+// Tiles over the blocks: as many whole rounds of tiles as there are, except that the last round
+// and a remainder after it (or all tiles, when they are fewer than the blocks) are cut along the
+// reduction into one run of groups of 4 blocks for each CTA, all of the same length: every SM
+// streams the same share of the weights although 16 tiles of a long reduction meet 148 SMs in a
+// decode step.  A tile cut into pieces is joined by the CTA that finishes last, from fp32
+// partial sums in the workspace, in the order of the reduction: equal inputs give equal bits.
 // Every wait is bounded as in the bf16 expert GEMM.
 #include <cuda_fp8.h>
 
@@ -82,9 +88,12 @@ struct Fp8Params {
   __nv_bfloat16* out;     // LINEAR: [rows, N]
   uint8_t* h;             // GATED: [rows, N] e4m3
   float* h_scale;         // GATED: [rows, nsb]
+  unsigned int* arrivals; // pieces of a cut tile that are done (0 between launches)
+  float* partials;        // [2 slots a CTA][half][128 rows][128 columns]
   DevStatus* status;
   uint64_t wait_ns;
 };
+constexpr int SLOT_FLOATS = 2 * BM * HALF_N;
 
 // acc += v * s for 16 columns of a thread's accumulator row, as packed pairs of fp32 FMAs.
 __device__ __forceinline__ void fma16(float2 (&acc)[64], int at, const uint32_t (&v)[16],
@@ -98,6 +107,15 @@ __device__ __forceinline__ void fma16(float2 (&acc)[64], int at, const uint32_t 
 }
 __device__ __forceinline__ float get(const float2 (&acc)[64], int i) {
   return i & 1 ? acc[i / 2].y : acc[i / 2].x;
+}
+
+// Programmatic dependent launch: let the next launch's blocks start as this one's leave their
+// SMs; wait until the launch before has completed (at once when there is none to wait for).
+__device__ __forceinline__ void let_next_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // 32 lanes x 16 columns of tensor memory, on their way until tmem_ld_wait().
@@ -183,6 +201,23 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return lo | (hi << 16);
 }
 
+// How a block of h is quantised, from its largest magnitude's bits.
+struct RowQuant {
+  float m, r;
+  bool bad;  // an infinity or a NaN in the block: NaN in all of it
+  __device__ __forceinline__ explicit RowQuant(uint32_t bits) {
+    bad = bits >= 0x7F800000u;
+    m = fmaxf(__uint_as_float(bits), 7.8886090522101181e-31f);  // 2^-100
+    r = __fdiv_rn(448.0f, m);
+  }
+  __device__ __forceinline__ uint32_t pack(float a, float b, float c, float d) const {
+    return bad ? 0x7F7F7F7Fu : e4m3x4(a * r, b * r, c * r, d * r);
+  }
+  __device__ __forceinline__ float scale() const {
+    return bad ? __uint_as_float(0x7FFFFFFFu) : __fdiv_rn(m, 448.0f);
+  }
+};
+
 // The bucket table of a launch in shared memory.
 struct Buckets {
   int start[MOE_MAX_EXPERTS];
@@ -219,6 +254,60 @@ __device__ void build_buckets(Buckets& t, const Fp8Params& p, int lane) {
   }
   if (lane == 0) t.tile_base[p.E] = carry * p.n_blocks;
 }
+
+// The work of one CTA: tiles, or pieces of tiles along the reduction.
+struct Piece {
+  int tile;
+  int kb0, kb1;  // its blocks of the reduction
+  int slot;      // -1: the whole tile; else where its partial sums go, 2 slots a CTA
+};
+
+struct Schedule {
+  int rounds;      // whole tiles this CTA takes: blockIdx.x + i * gridDim.x
+  int cut_tiles;   // tiles from rounds * gridDim.x on that are cut
+  int groups;      // groups of 4 blocks of a tile
+  int ctas;        // that share them
+  int64_t units;   // cut_tiles * groups
+
+  __device__ Schedule(int total, int KB) {
+    const int G = static_cast<int>(gridDim.x);
+    const int full = total / G, rest = total - full * G;
+    // cutting pays when the last round would leave a tenth of the SMs' time unused
+    const bool cut = rest != 0 && static_cast<int64_t>(full + 1) * G * 10 > static_cast<int64_t>(total) * 11;
+    rounds = cut ? (full > 0 ? full - 1 : 0) : full + (static_cast<int>(blockIdx.x) < rest ? 1 : 0);
+    cut_tiles = cut ? total - rounds * G : 0;
+    groups = (KB + 3) >> 2;
+    units = static_cast<int64_t>(cut_tiles) * groups;
+    ctas = units < G ? static_cast<int>(units) : G;
+  }
+  // first unit of CTA c, and the CTA that has unit u
+  __device__ int64_t begin(int c) const { return units * c / ctas; }
+  __device__ int owner(int64_t u) const { return static_cast<int>(((u + 1) * ctas - 1) / units); }
+  // The i-th piece of this CTA (i counts up from 0); false past the last.
+  __device__ bool get(int i, int KB, Piece& w) const {
+    if (i < rounds) {
+      w.tile = static_cast<int>(blockIdx.x + static_cast<unsigned>(i) * gridDim.x);
+      w.kb0 = 0;
+      w.kb1 = KB;
+      w.slot = -1;
+      return true;
+    }
+    const int c = static_cast<int>(blockIdx.x);
+    if (c >= ctas) return false;
+    const int64_t u0 = begin(c), u1 = begin(c + 1);
+    const int first = static_cast<int>(u0 / groups);
+    const int t = first + i - rounds;
+    const int64_t t0 = static_cast<int64_t>(t) * groups;
+    if (t0 >= u1) return false;
+    const int g0 = t0 < u0 ? static_cast<int>(u0 - t0) : 0;
+    const int g1 = u1 - t0 < groups ? static_cast<int>(u1 - t0) : groups;
+    w.tile = rounds * static_cast<int>(gridDim.x) + t;
+    w.kb0 = 4 * g0;
+    w.kb1 = min(KB, 4 * g1);
+    w.slot = g0 == 0 && g1 == groups ? -1 : 2 * c + (t == first ? 0 : 1);
+    return true;
+  }
+};
 
 struct Tile {
   int e, nb, row0, valid;  // expert, column block, first row, rows from there in the bucket
@@ -279,6 +368,8 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
   __shared__ __align__(8) uint64_t sfull_bar[2];         // 4 blocks' scales are there
   __shared__ __align__(8) uint64_t sfree_bar[2];         // ... and have been read
   __shared__ __align__(8) uint64_t amax_bar;
+  __shared__ __align__(8) uint64_t join_bar[2];          // partial sums written; who was last
+  __shared__ int last_s;
   __shared__ __align__(8) uint64_t drain_bar[2];
   __shared__ uint32_t tmem_base_s;
   __shared__ volatile int abort_s;
@@ -315,6 +406,8 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
       mbar_init(&drain_bar[i], 1);
     }
     mbar_init(&amax_bar, EPI_WARPS);
+    mbar_init(&join_bar[0], EPI_WARPS);
+    mbar_init(&join_bar[1], 1);
     abort_s = 0;
     fence_barrier_init();
   }
@@ -322,9 +415,11 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
   __syncthreads();
   tc_fence_after();
 
+  if (GATED) let_next_start();  // the down product's blocks: they wait before they read h
   const uint32_t tmem_base = tmem_base_s;
   const int total = bk.tile_base[p.E];
   const int KB = p.kb;
+  const Schedule sched(total, KB);
 
   // The whole warp waits for a barrier.  Once a wait has run out, here or elsewhere in the
   // block, every role's next wait fails and the roles unwind.
@@ -345,46 +440,64 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
     regs_dec<CTRL_REGS>();
     uint32_t fills = 0;  // bit s: parity of stage s's next fill
     uint32_t armed = 0, armed_parity = 0;
-    bool ok = true;
-    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+    bool ok = true, waited = false;
+    int early = 0;  // blocks of the first piece whose weights were loaded ahead
+    Piece w;
+    for (int i = 0; ok && sched.get(i, KB, w); ++i) {
+      const int tile = w.tile;
       const Tile t = decode(bk, p, tile);
       const int groups = t.valid > BM - 32 ? BM / 32 : (t.valid + 31) >> 5;  // of 32 rows
-#pragma unroll 1
-      for (int kb = 0; kb < KB; ++kb) {
-          const int s = kb & (STAGES - 1);
-          const uint32_t par = (fills >> s) & 1u;
-          if (!await(&done_bar[0][s], par ^ 1u, 41, tile) ||
-              !await(&done_bar[1][s], par ^ 1u, 41, tile)) {
-            ok = false;
-            break;
-          }
-          uint8_t* sa = smem + s * STAGE_BYTES;
-          uint8_t* sb = sa + A_BYTES;
-          if (elect_one()) {
-            mbar_arrive_expect_tx(&full_bar[s], B_BYTES + groups * 32 * BK);
-            if (GATED) {
+      auto load_weights = [&](int kb) {
+        const int s = kb & (STAGES - 1);
+        uint8_t* sb = smem + s * STAGE_BYTES + A_BYTES;
+        mbar_arrive_expect_tx(&full_bar[s], B_BYTES + groups * 32 * BK);
+        if (GATED) {
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                uint8_t* to = sb + h * HALF_N * BK;
-                tma_load_3d(to, &tm_b0, &full_bar[s], kb * BK, t.nb * 128 + h * 64, t.e);
-                tma_load_3d(to + 64 * BK, &tm_b1, &full_bar[s], kb * BK, t.nb * 128 + h * 64, t.e);
-              }
-            } else {
-              tma_load_3d(sb, &tm_b0, &full_bar[s], kb * BK, t.nb * BN, t.e);
-            }
-            if (groups == 4) {
-              tma_load_2d(sa, &tm_a, &full_bar[s], kb * BK, t.row0);
-            } else {
-              for (int g = 0; g < groups; ++g)
-                tma_load_2d(sa + g * 32 * BK, &tm_a32, &full_bar[s], kb * BK, t.row0 + g * 32);
-            }
+          for (int h = 0; h < 2; ++h) {
+            uint8_t* to = sb + h * HALF_N * BK;
+            tma_load_3d(to, &tm_b0, &full_bar[s], kb * BK, t.nb * 128 + h * 64, t.e);
+            tma_load_3d(to + 64 * BK, &tm_b1, &full_bar[s], kb * BK, t.nb * 128 + h * 64, t.e);
           }
-          __syncwarp();
-          armed |= 1u << s;
-          armed_parity = (armed_parity & ~(1u << s)) | (par << s);
-          fills ^= 1u << s;
+        } else {
+          tma_load_3d(sb, &tm_b0, &full_bar[s], kb * BK, t.nb * BN, t.e);
+        }
+      };
+      if (!waited) {  // the weights of the first blocks do not depend on the launch before
+        early = min(STAGES, w.kb1 - w.kb0);
+        if (elect_one())
+          for (int kb = w.kb0; kb < w.kb0 + early; ++kb) load_weights(kb);
+        __syncwarp();
+        wait_for_previous();
+        waited = true;
+      }
+#pragma unroll 1
+      for (int kb = w.kb0; kb < w.kb1; ++kb) {
+        const int s = kb & (STAGES - 1);
+        const uint32_t par = (fills >> s) & 1u;
+        const bool ahead = early > 0;
+        if (!ahead && (!await(&done_bar[0][s], par ^ 1u, 41, tile) ||
+                       !await(&done_bar[1][s], par ^ 1u, 41, tile))) {
+          ok = false;
+          break;
+        }
+        uint8_t* sa = smem + s * STAGE_BYTES;
+        if (elect_one()) {
+          if (!ahead) load_weights(kb);
+          if (groups == 4) {
+            tma_load_2d(sa, &tm_a, &full_bar[s], kb * BK, t.row0);
+          } else {
+            for (int g = 0; g < groups; ++g)
+              tma_load_2d(sa + g * 32 * BK, &tm_a32, &full_bar[s], kb * BK, t.row0 + g * 32);
+          }
+        }
+        __syncwarp();
+        if (ahead) --early;
+        armed |= 1u << s;
+        armed_parity = (armed_parity & ~(1u << s)) | (par << s);
+        fills ^= 1u << s;
       }
     }
+    if (!waited) wait_for_previous();
     // every fill must land before the block can exit
     for (int s = 0; s < STAGES; ++s)
       if ((armed >> s) & 1u)
@@ -393,15 +506,18 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
   } else if (warp < 3) {
     // ---------------------------------------------------------------- MMA issuers
     regs_dec<CTRL_REGS>();
+    wait_for_previous();
     constexpr uint32_t idesc = idesc_e4m3_f32(BM, HALF_N);
     const int h = warp - 1;
     const uint64_t a_desc = sw128_kmajor_desc(smem_addr(smem));
     const uint64_t b_desc = sw128_kmajor_desc(smem_addr(smem) + A_BYTES + h * HALF_N * BK);
     uint32_t fills = 0, uses = 0;  // parities: stage s's next fill, accumulator j's next use
     bool ok = true, issued = false;
-    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+    Piece w;
+    for (int i = 0; ok && sched.get(i, KB, w); ++i) {
+      const int tile = w.tile;
 #pragma unroll 1
-      for (int kb = 0; kb < KB; ++kb) {
+      for (int kb = w.kb0; kb < w.kb1; ++kb) {
           const int s = kb & (STAGES - 1), j = kb & 1;
           if (!await(&full_bar[s], (fills >> s) & 1u, 42, tile) ||
               !await(&tempty_bar[h][j], ((uses >> j) & 1u) ^ 1u, 42, tile)) {
@@ -431,11 +547,14 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
   } else if (warp == 3) {
     // ---------------------------------------------------------------- scales
     regs_dec<CTRL_REGS>();
+    wait_for_previous();
     // A lane has rows lane + 32 i of the tile.  (The epilogue's threads loading their own rows'
     // scales took a fifth of its time: 32 rows' lanes are 32 passes of the L1.)
     uint32_t turns = 0;  // of 4 blocks, over all tiles
     bool ok = true;
-    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+    Piece w;
+    for (int i = 0; ok && sched.get(i, KB, w); ++i) {
+      const int tile = w.tile;
       const Tile t = decode(bk, p, tile);
       const float* sa = p.a_scale + (static_cast<int64_t>(t.row0) + lane) * KB;
       const int64_t w_row = static_cast<int64_t>(t.e) * p.nsb;
@@ -443,12 +562,12 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
       const float* s0 = p.w_scale0 + (w_row + (GATED ? t.nb : 2 * t.nb)) * KB;
       const float* s1 = GATED ? p.w_scale1 + (w_row + t.nb) * KB
                               : p.w_scale0 + (w_row + min(2 * t.nb + 1, p.nsb - 1)) * KB;
-      for (int k0 = 0; k0 < KB; k0 += 4) {
+      for (int k0 = w.kb0; k0 < w.kb1; k0 += 4) {
         float4 a[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          a[i] = lane + 32 * i < t.valid
-                     ? scales4(sa + static_cast<int64_t>(32 * i) * KB, k0, KB)
+        for (int m = 0; m < 4; ++m)
+          a[m] = lane + 32 * m < t.valid
+                     ? scales4(sa + static_cast<int64_t>(32 * m) * KB, k0, KB)
                      : make_float4(0.f, 0.f, 0.f, 0.f);
         const float4 w0 = scales4(s0, k0, KB), w1 = scales4(s1, k0, KB);
         const uint32_t b = turns & 1u;
@@ -459,9 +578,9 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            scale_s[b][k][0][lane + 32 * i] = pick(a[i], k) * pick(w0, k);
-            scale_s[b][k][1][lane + 32 * i] = pick(a[i], k) * pick(w1, k);
+          for (int m = 0; m < 4; ++m) {
+            scale_s[b][k][0][lane + 32 * m] = pick(a[m], k) * pick(w0, k);
+            scale_s[b][k][1][lane + 32 * m] = pick(a[m], k) * pick(w1, k);
           }
         __syncwarp();
         arrive_if(&sfull_bar[b], lane == 0);
@@ -471,6 +590,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
   } else {
     // ---------------------------------------------------------------- epilogue
     regs_inc<EPI_REGS>();
+    wait_for_previous();
     const int q = warp & 3;                     // TMEM lane quarter this warp may access
     const int half = (warp - CTRL_WARPS) >> 2;  // which half's accumulators
     const int r = q * 32 + lane;                // accumulator row of this thread
@@ -479,16 +599,18 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
                         static_cast<uint32_t>(2 * half * HALF_N);
     uint8_t* stage_out = smem + STAGES * STAGE_BYTES + (warp - CTRL_WARPS) * OUT_STAGE;
     uint32_t fills = 0;  // bit s: parity of stage s's next fill
-    uint32_t turns = 0, xph = 0;
+    uint32_t turns = 0, xph = 0, jph = 0;
     bool ok = true;
-    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+    Piece w;
+    for (int i = 0; ok && sched.get(i, KB, w); ++i) {
+      const int tile = w.tile;
       const Tile t = decode(bk, p, tile);
       const bool live = 32 * q < t.valid;  // the warp has bucket rows
       float2 acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
 #pragma unroll 1
-      for (int kb = 0; kb < KB; ++kb) {
+      for (int kb = w.kb0; kb < w.kb1; ++kb) {
         const int s = kb & (STAGES - 1), j = kb & 1;
         const uint32_t b = turns & 1u;
         if (s == 0 && !await(&sfull_bar[b], (turns >> 1) & 1u, 46, tile)) {
@@ -521,7 +643,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
         } else {
           arrive_if(&tempty_bar[half][j], first);
         }
-        if (s == STAGES - 1 || kb == KB - 1) {  // every lane has read the 4 blocks' scales
+        if (s == STAGES - 1 || kb == w.kb1 - 1) {  // every lane has read the 4 blocks' scales
           __syncwarp();
           arrive_if(&sfree_bar[b], first);
           ++turns;
@@ -529,6 +651,114 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
       }
       if (!ok) break;
       const int left = t.valid - 32 * q;  // rows of this warp, from its first
+      if (w.slot >= 0) {
+        // a piece: its sums go to the workspace; the CTA whose piece of the tile is the last to
+        // arrive there adds all of them up, first piece first
+        if (lane < left) {
+          float4* to = reinterpret_cast<float4*>(
+              p.partials + static_cast<int64_t>(w.slot) * SLOT_FLOATS + (half * BM + r) * HALF_N);
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            __stcg(to + c, make_float4(acc[2 * c].x, acc[2 * c].y, acc[2 * c + 1].x,
+                                       acc[2 * c + 1].y));
+        }
+        const int cut = tile - sched.rounds * static_cast<int>(gridDim.x);
+        const int64_t tile0 = static_cast<int64_t>(cut) * sched.groups;
+        // its pieces' CTAs; each has the tile as its run's first, but for the first of them when
+        // that one's run starts in a tile before
+        const int c0 = sched.owner(tile0), c1 = sched.owner(tile0 + sched.groups - 1);
+        const bool starts = sched.begin(c0) == tile0;
+        __threadfence();
+        __syncwarp();
+        arrive_if(&join_bar[0], first);
+        if (warp == CTRL_WARPS) {
+          if (!await(&join_bar[0], jph, 47, tile)) break;
+          if (lane == 0) {
+            __threadfence();
+            const unsigned before = atomicAdd(p.arrivals + cut, 1u);
+            const int is_last = before == static_cast<unsigned>(c1 - c0);
+            if (is_last) p.arrivals[cut] = 0u;  // as the next launch wants it
+            __threadfence();
+            last_s = is_last;
+          }
+          __syncwarp();
+          arrive_if(&join_bar[1], first);
+        }
+        if (!await(&join_bar[1], jph, 48, tile)) break;
+        jph ^= 1u;
+        if (last_s != 0) {
+          __threadfence();
+          // A warp takes every second of its quarter's rows, 4 at a time, and a lane 4 columns
+          // of each half: a row's 1 KB is read at once, where a thread with a row to itself
+          // would wait for memory 32 times as often.
+#pragma unroll 1
+          for (int m0 = half; m0 < 32 && m0 < left; m0 += 8) {
+            float4 v[4][2];
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+              v[m][0] = v[m][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+            for (int c = c0; c <= c1; ++c) {
+              const int slot = 2 * c + (c == c0 && !starts ? 1 : 0);
+              const float4* from =
+                  reinterpret_cast<const float4*>(
+                      p.partials + static_cast<int64_t>(slot) * SLOT_FLOATS +
+                      (32 * q + m0) * HALF_N) + lane;
+#pragma unroll
+              for (int m = 0; m < 4; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  if (m0 + 2 * m < left) {
+                    const float4 x = __ldcg(from + (h * BM + 2 * m) * HALF_N / 4);
+                    v[m][h].x += x.x;
+                    v[m][h].y += x.y;
+                    v[m][h].z += x.z;
+                    v[m][h].w += x.w;
+                  }
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              if (m0 + 2 * m >= left) break;
+              const int64_t row = static_cast<int64_t>(t.row0) + 32 * q + m0 + 2 * m;
+              if (GATED) {  // lanes 0-15 have 4 gate columns, lanes 16-31 the same of up
+                uint32_t most = 0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  float* e = reinterpret_cast<float*>(&v[m][h]);
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    const float other = __shfl_xor_sync(0xffffffffu, e[k], 16);
+                    e[k] = silu_mul(lane < 16 ? e[k] : other, lane < 16 ? other : e[k]);
+                    most = max(most, __float_as_uint(e[k]) & 0x7FFFFFFFu);
+                  }
+                }
+                most = __reduce_max_sync(0xffffffffu, most);
+                const RowQuant rq(most);
+                if (lane < 16) {
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    const int col = t.nb * 128 + 64 * h + 4 * lane;
+                    if (col < p.N)
+                      *reinterpret_cast<uint32_t*>(p.h + row * p.N + col) =
+                          rq.pack(v[m][h].x, v[m][h].y, v[m][h].z, v[m][h].w);
+                  }
+                }
+                if (lane == 0) p.h_scale[row * p.nsb + t.nb] = rq.scale();
+              } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const int col = t.nb * BN + HALF_N * h + 4 * lane;
+                  if (col < p.N)
+                    *reinterpret_cast<uint2*>(p.out + row * p.N + col) =
+                        make_uint2(pack_bf16x2(v[m][h].x, v[m][h].y),
+                                   pack_bf16x2(v[m][h].z, v[m][h].w));
+                }
+              }
+            }
+          }
+        }
+        continue;
+      }
       if (GATED) {
         // h of this thread's 64 columns over its gate half of the accumulators, the row's
         // largest magnitude over both halves, then e4m3 and the scale
@@ -550,22 +780,17 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
         m = max(m, amax_s[xph][half ^ 1][r]);
         xph ^= 1u;
         if (live) {
-          const bool bad = m >= 0x7F800000u;
-          const float mf = fmaxf(__uint_as_float(m), 7.8886090522101181e-31f);  // 2^-100
-          const float rs = __fdiv_rn(448.0f, mf);
+          const RowQuant rq(m);
           uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            w[i] = e4m3x4(acc[2 * i].x * rs, acc[2 * i].y * rs, acc[2 * i + 1].x * rs,
-                          acc[2 * i + 1].y * rs);
-            if (bad) w[i] = 0x7F7F7F7Fu;
-          }
+          for (int i = 0; i < 16; ++i)
+            w[i] = rq.pack(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
           const int col = t.nb * 128 + 64 * half;
           store_rows64(stage_out, w, p.h + (static_cast<int64_t>(t.row0) + 32 * q) * p.N + col,
                        p.N, left, p.N - col, lane);
           if (half == 0 && lane < left)
             p.h_scale[(static_cast<int64_t>(t.row0) + r) * p.nsb + t.nb] =
-                bad ? __uint_as_float(0x7FFFFFFFu) : __fdiv_rn(mf, 448.0f);
+                rq.scale();
         }
       } else if (live) {
         const int col = t.nb * BN + HALF_N * half;
@@ -624,22 +849,34 @@ bool map_weights(CUtensorMap* m, const void* base, int64_t E, int64_t N, int64_t
 
 template <int MODE>
 cudaError_t launch(const CUtensorMap& a, const CUtensorMap& a32, const CUtensorMap& b0,
-                   const CUtensorMap& b1, const Fp8Params& p, cudaStream_t st) {
+                   const CUtensorMap& b1, const Fp8Params& p, bool follows, cudaStream_t st) {
   cudaError_t err = cudaFuncSetAttribute(fp8_grouped_gemm_kernel<MODE>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, DYN_SMEM);
   if (err != cudaSuccess) return err;
   // at most one ragged row block per bucket, the rest full
   int64_t tiles = (p.rows / BM + (p.rows < p.E ? p.rows : p.E)) * p.n_blocks;
+  tiles *= (p.kb + 3) / 4;  // a tile can be cut into that many pieces
   if (tiles > sm_count()) tiles = sm_count();
-  fp8_grouped_gemm_kernel<MODE><<<static_cast<unsigned>(tiles), THREADS, DYN_SMEM, st>>>(
-      a, a32, b0, b1, p);
-  note_launch();
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = DYN_SMEM;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = follows ? 1 : 0;
+  err = cudaLaunchKernelEx(&cfg, fp8_grouped_gemm_kernel<MODE>, a, a32, b0, b1, p);
+  if (err == cudaSuccess) note_launch();
+  return err;
 }
 
 }  // namespace
 
-size_t fp8_workspace_bytes() { return kFp8PartialsOffset; }
+size_t fp8_workspace_bytes() {
+  return kFp8PartialsOffset + sizeof(float) * SLOT_FLOATS * 2 * static_cast<size_t>(sm_count());
+}
 
 cudaError_t launch_fp8_gemm(const Fp8Gemm& g, void* ws, uint64_t wait_ns, cudaStream_t st,
                             const char** why) {
@@ -673,9 +910,12 @@ cudaError_t launch_fp8_gemm(const Fp8Gemm& g, void* ws, uint64_t wait_ns, cudaSt
   p.out = static_cast<__nv_bfloat16*>(g.out);
   p.h = static_cast<uint8_t*>(g.h);
   p.h_scale = g.h_scale;
+  p.arrivals = reinterpret_cast<unsigned int*>(static_cast<uint8_t*>(ws) + kFp8CountersOffset);
+  p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kFp8PartialsOffset);
   p.status = static_cast<DevStatus*>(ws);
   p.wait_ns = wait_ns;
-  return gated ? launch<FP8_GATED>(a, a32, b0, b1, p, st) : launch<FP8_LINEAR>(a, a32, b0, b1, p, st);
+  return gated ? launch<FP8_GATED>(a, a32, b0, b1, p, g.follows, st)
+               : launch<FP8_LINEAR>(a, a32, b0, b1, p, g.follows, st);
 }
 
 }  // namespace moe

@@ -186,6 +186,8 @@ struct Fp8Gemm {
   void* out;                // [rows, N] bf16
   void* h;                  // [rows, N] e4m3
   float* h_scale;           // [rows, ceil(N / 128)]
+  bool follows;             // the launch before in the stream is the product that made a: this
+                            // one's blocks may start as that one's end
 };
 // Workspace of the fp8 products: the status record, then arrival counters (zero between
 // calls), then partial sums.

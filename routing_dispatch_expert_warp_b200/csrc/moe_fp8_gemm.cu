@@ -35,11 +35,10 @@
 // A hand-over between an MMA issuer and an epilogue takes some 200 cycles each way.  With the
 // halves apart, four accumulators of 128 columns are on their way round instead of two of 256,
 // and one half's epilogue computes while the other's waits.
-// Tiles over the blocks: as many whole rounds of tiles as there are, except that the last round
-// and a remainder after it (or all tiles, when they are fewer than the blocks) are cut along the
-// reduction into one run of groups of 4 blocks for each CTA, all of the same length: every SM
-// streams the same share of the weights although 16 tiles of a long reduction meet 148 SMs in a
-// decode step.  A tile cut into pieces is joined by the CTA that finishes last, from fp32
+// Tiles over the blocks: whole tiles in rounds, or, when there are few of them, all tiles cut
+// along the reduction into one run of groups of 4 blocks for each CTA, all of the same length:
+// every SM streams the same share of the weights although 16 tiles of a long reduction meet 148
+// SMs in a decode step.  A tile cut into pieces is joined by the CTA that finishes last, from fp32
 // partial sums in the workspace, in the order of the reduction: equal inputs give equal bits.
 // Every wait is bounded as in the bf16 expert GEMM.
 #include <cuda_fp8.h>
@@ -264,7 +263,7 @@ struct Piece {
 
 struct Schedule {
   int rounds;      // whole tiles this CTA takes: blockIdx.x + i * gridDim.x
-  int cut_tiles;   // tiles from rounds * gridDim.x on that are cut
+  int cut_tiles;   // all tiles, or none, are cut
   int groups;      // groups of 4 blocks of a tile
   int ctas;        // that share them
   int64_t units;   // cut_tiles * groups
@@ -272,10 +271,14 @@ struct Schedule {
   __device__ Schedule(int total, int KB) {
     const int G = static_cast<int>(gridDim.x);
     const int full = total / G, rest = total - full * G;
-    // cutting pays when the last round would leave a tenth of the SMs' time unused
-    const bool cut = rest != 0 && static_cast<int64_t>(full + 1) * G * 10 > static_cast<int64_t>(total) * 11;
-    rounds = cut ? (full > 0 ? full - 1 : 0) : full + (static_cast<int>(blockIdx.x) < rest ? 1 : 0);
-    cut_tiles = cut ? total - rounds * G : 0;
+    // Cut only when there are fewer than two whole rounds and the last would leave a tenth of
+    // the SMs' time unused.  (One token of the Mixtral-8x7B shaped layer, 224 and 32 tiles: 104
+    // us whole, 80 us cut.  With more rounds the SMs idle in the last one save power that the
+    // others use, and the joins cost more than they gain: 4096 x 4096 x 7168, 512 tiles: 129 us
+    // whole, 137 us cut.)
+    const bool cut = full < 2 && rest != 0 && (full + 1) * G * 10 > total * 11;
+    rounds = cut ? 0 : full + (static_cast<int>(blockIdx.x) < rest ? 1 : 0);
+    cut_tiles = cut ? total : 0;
     groups = (KB + 3) >> 2;
     units = static_cast<int64_t>(cut_tiles) * groups;
     ctas = units < G ? static_cast<int>(units) : G;
@@ -301,7 +304,7 @@ struct Schedule {
     if (t0 >= u1) return false;
     const int g0 = t0 < u0 ? static_cast<int>(u0 - t0) : 0;
     const int g1 = u1 - t0 < groups ? static_cast<int>(u1 - t0) : groups;
-    w.tile = rounds * static_cast<int>(gridDim.x) + t;
+    w.tile = t;
     w.kb0 = 4 * g0;
     w.kb1 = min(KB, 4 * g1);
     w.slot = g0 == 0 && g1 == groups ? -1 : 2 * c + (t == first ? 0 : 1);
@@ -662,7 +665,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
             __stcg(to + c, make_float4(acc[2 * c].x, acc[2 * c].y, acc[2 * c + 1].x,
                                        acc[2 * c + 1].y));
         }
-        const int cut = tile - sched.rounds * static_cast<int>(gridDim.x);
+        const int cut = tile;
         const int64_t tile0 = static_cast<int64_t>(cut) * sched.groups;
         // its pieces' CTAs; each has the tile as its run's first, but for the first of them when
         // that one's run starts in a tile before

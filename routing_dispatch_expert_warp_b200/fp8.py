@@ -43,11 +43,11 @@ def fp8_scale_shape(shape) -> tuple:
 
 def _need(t, name: str, dtype, shape, device) -> int:
     """The address of a contiguous tensor of this type, shape and device."""
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
-                         f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}"
-                         f"{'' if t.is_contiguous() else ', not contiguous'}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                     f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}"
+                     f"{'' if t.is_contiguous() else ', not contiguous'}")
 
 
 def _source(t, name: str, axes: int) -> int:
@@ -57,27 +57,32 @@ def _source(t, name: str, axes: int) -> int:
     return t.data_ptr()
 
 
+# The handle of a device's current stream; torch.cuda.current_stream takes some 2 us to say it,
+# as long as a launch.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _call(fn, device: torch.device, stream, *args) -> None:
     """fn(*args, stream) with the tensors' device current."""
+    index = device.index
     if device.type != "cuda":
         raise ValueError(f"the tensors must be on a CUDA device, got {device}")
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            _enqueue(fn, device, stream, args)
-    else:
-        _enqueue(fn, device, stream, args)
-
-
-def _enqueue(fn, device, stream, args) -> None:
     if stream is None:
-        raw = torch.cuda.current_stream(device).cuda_stream
+        raw = _raw_stream(index)
     elif isinstance(stream, torch.cuda.Stream):
         if stream.device != device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
         raw = stream.cuda_stream
     else:
         raw = int(stream)
-    check(fn(*args, raw))
+    if index == torch.cuda.current_device():
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, raw)
+    if status:
+        check(status)
 
 
 def _max_rows(cfg: MoeConfig) -> int:

@@ -235,6 +235,9 @@ GEMM = [  # counts, N, K
     ([0, 0], 256, 256),
     ([1, 1], 4096, 14336),
     ([260, 513, 1, 255, 256, 257], 768, 640),
+    ([200, 0, 0, 1, 0, 0, 17, 0], 1000, 1520),   # one long bucket among few rows
+    ([64, 16, 15, 17, 48, 49, 63, 65, 0, 1, 0, 2], 520, 272),
+    ([5], 14336, 4096),
 ]
 
 
@@ -334,6 +337,9 @@ FFN = [  # counts, d, f
     ([1] * 40, 384, 144),
     ([33, 0, 257, 129], 640, 1008),
     ([2, 3], 4096, 1024),
+    ([200, 0, 0, 1, 0, 0, 17, 0], 272, 400),
+    ([2, 0, 0, 0, 1, 0], 1520, 2064),
+    ([1], 4096, 14336),
 ]
 
 

@@ -36,8 +36,67 @@ constexpr int TMEM_COLS = 512;         // 4 stages x 2 halves x 64
 constexpr int OUT_ROWS = 16;           // bucket rows on their way through shared memory
 constexpr int OUT_BYTES = OUT_ROWS * BN * 4;
 constexpr int DYN_SMEM = STAGES * STAGE_BYTES + 2 * OUT_BYTES + 1024;  // + alignment
-// partial sums of a piece: [64 bucket rows][256 weight rows]
-static_assert(TM * BN <= SLOT_FLOATS, "a piece has to fit its slot");
+static_assert(SLOT_FLOATS == TM * BN, "partial sums of a piece: [64 bucket rows][256 weight rows]");
+
+// The work of one CTA: tiles, or pieces of tiles along the reduction.
+struct Piece {
+  int tile;
+  int kb0, kb1;  // its blocks of the reduction
+  int slot;      // -1: the whole tile; else where its partial sums go, 2 slots a CTA
+};
+
+struct Schedule {
+  int rounds;      // whole tiles this CTA takes: blockIdx.x + i * gridDim.x
+  int cut_tiles;   // all tiles, or none, are cut
+  int groups;      // groups of 4 blocks of a tile
+  int ctas;        // that share them
+  int64_t units;   // cut_tiles * groups
+
+  __device__ Schedule(int total, int KB) {
+    const int G = static_cast<int>(gridDim.x);
+    const int full = total / G, rest = total - full * G;
+    // Cutting saves the blocks of the reduction that the last round leaves unused and costs a
+    // join, as long as some 14 of a tile's blocks.  (One row, N = 4096, K = 4096, 16 tiles, 28
+    // blocks saved: 19.1 us whole, 11.7 cut.  16 rows, 7168, 2048, 13 saved: 12.9 and 13.0.  8
+    // experts' rows, 7168, 2048, 8 saved: 29.2 and 32.0.)
+    constexpr int join_blocks = 14;
+    const bool cut = full < 2 && rest != 0 &&
+                     static_cast<int64_t>((full + 1) * G - total) * KB >
+                         static_cast<int64_t>(join_blocks) * G;
+    rounds = cut ? 0 : full + (static_cast<int>(blockIdx.x) < rest ? 1 : 0);
+    cut_tiles = cut ? total : 0;
+    groups = (KB + 3) >> 2;
+    units = static_cast<int64_t>(cut_tiles) * groups;
+    ctas = units < G ? static_cast<int>(units) : G;
+  }
+  // first unit of CTA c, and the CTA that has unit u
+  __device__ int64_t begin(int c) const { return units * c / ctas; }
+  __device__ int owner(int64_t u) const { return static_cast<int>(((u + 1) * ctas - 1) / units); }
+  // The i-th piece of this CTA (i counts up from 0); false past the last.
+  __device__ bool get(int i, int KB, Piece& w) const {
+    if (i < rounds) {
+      w.tile = static_cast<int>(blockIdx.x + static_cast<unsigned>(i) * gridDim.x);
+      w.kb0 = 0;
+      w.kb1 = KB;
+      w.slot = -1;
+      return true;
+    }
+    const int c = static_cast<int>(blockIdx.x);
+    if (c >= ctas) return false;
+    const int64_t u0 = begin(c), u1 = begin(c + 1);
+    const int first = static_cast<int>(u0 / groups);
+    const int t = first + i - rounds;
+    const int64_t t0 = static_cast<int64_t>(t) * groups;
+    if (t0 >= u1) return false;
+    const int g0 = t0 < u0 ? static_cast<int>(u0 - t0) : 0;
+    const int g1 = u1 - t0 < groups ? static_cast<int>(u1 - t0) : groups;
+    w.tile = t;
+    w.kb0 = 4 * g0;
+    w.kb1 = min(KB, 4 * g1);
+    w.slot = g0 == 0 && g1 == groups ? -1 : 2 * c + (t == first ? 0 : 1);
+    return true;
+  }
+};
 
 // One bucket row of a tile: the lane's sums of weight rows 4 lane .. + 3 of either half.
 template <int MODE>

@@ -35,11 +35,9 @@
 // A hand-over between an MMA issuer and an epilogue takes some 200 cycles each way.  With the
 // halves apart, four accumulators of 128 columns are on their way round instead of two of 256,
 // and one half's epilogue computes while the other's waits.
-// Tiles over the blocks: whole tiles in rounds, or, when there are few of them, all tiles cut
-// along the reduction into one run of groups of 4 blocks for each CTA, all of the same length:
-// every SM streams the same share of the weights although 16 tiles of a long reduction meet 148
-// SMs in a decode step.  A tile cut into pieces is joined by the CTA that finishes last, from fp32
-// partial sums in the workspace, in the order of the reduction: equal inputs give equal bits.
+// (Tiles are not cut along the reduction when they are fewer than the SMs: a cut tile's 128 KB
+// of partial sums and their join take as long as 60 to 75 of its blocks.  256 x 4096 x 14336, 32
+// tiles: 60 us whole, 55 cut; 384 x 7168 x 2048: 17 us whole, 41 cut.)
 // Every wait is bounded as in the bf16 expert GEMM.
 #include "moe_fp8_gemm.cuh"
 
@@ -119,8 +117,6 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
   __shared__ __align__(8) uint64_t sfull_bar[2];         // 4 blocks' scales are there
   __shared__ __align__(8) uint64_t sfree_bar[2];         // ... and have been read
   __shared__ __align__(8) uint64_t amax_bar;
-  __shared__ __align__(8) uint64_t join_bar[2];          // partial sums written; who was last
-  __shared__ int last_s;
   __shared__ __align__(8) uint64_t drain_bar[2];
   __shared__ uint32_t tmem_base_s;
   __shared__ volatile int abort_s;
@@ -157,8 +153,6 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
       mbar_init(&drain_bar[i], 1);
     }
     mbar_init(&amax_bar, EPI_WARPS);
-    mbar_init(&join_bar[0], EPI_WARPS);
-    mbar_init(&join_bar[1], 1);
     abort_s = 0;
     fence_barrier_init();
   }
@@ -170,7 +164,6 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
   const uint32_t tmem_base = tmem_base_s;
   const int total = bk.tile_base[p.E];
   const int KB = p.kb;
-  const Schedule sched(total, KB);
 
   // The whole warp waits for a barrier.  Once a wait has run out, here or elsewhere in the
   // block, every role's next wait fails and the roles unwind.
@@ -192,10 +185,8 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
     uint32_t fills = 0;  // bit s: parity of stage s's next fill
     uint32_t armed = 0, armed_parity = 0;
     bool ok = true, waited = false;
-    int early = 0;  // blocks of the first piece whose weights were loaded ahead
-    Piece w;
-    for (int i = 0; ok && sched.get(i, KB, w); ++i) {
-      const int tile = w.tile;
+    int early = 0;  // blocks of the first tile whose weights were loaded ahead
+    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
       const Tile t = decode<BM>(bk, p, tile);
       const int groups = t.valid > BM - 32 ? BM / 32 : (t.valid + 31) >> 5;  // of 32 rows
       auto load_weights = [&](int kb) {
@@ -214,15 +205,15 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
         }
       };
       if (!waited) {  // the weights of the first blocks do not depend on the launch before
-        early = min(STAGES, w.kb1 - w.kb0);
+        early = min(STAGES, KB);
         if (elect_one())
-          for (int kb = w.kb0; kb < w.kb0 + early; ++kb) load_weights(kb);
+          for (int kb = 0; kb < early; ++kb) load_weights(kb);
         __syncwarp();
         wait_for_previous();
         waited = true;
       }
 #pragma unroll 1
-      for (int kb = w.kb0; kb < w.kb1; ++kb) {
+      for (int kb = 0; kb < KB; ++kb) {
         const int s = kb & (STAGES - 1);
         const uint32_t par = (fills >> s) & 1u;
         const bool ahead = early > 0;
@@ -264,11 +255,9 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
     const uint64_t b_desc = sw128_kmajor_desc(smem_addr(smem) + A_BYTES + h * HALF_N * BK);
     uint32_t fills = 0, uses = 0;  // parities: stage s's next fill, accumulator j's next use
     bool ok = true, issued = false;
-    Piece w;
-    for (int i = 0; ok && sched.get(i, KB, w); ++i) {
-      const int tile = w.tile;
+    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
 #pragma unroll 1
-      for (int kb = w.kb0; kb < w.kb1; ++kb) {
+      for (int kb = 0; kb < KB; ++kb) {
           const int s = kb & (STAGES - 1), j = kb & 1;
           if (!await(&full_bar[s], (fills >> s) & 1u, 42, tile) ||
               !await(&tempty_bar[h][j], ((uses >> j) & 1u) ^ 1u, 42, tile)) {
@@ -303,9 +292,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
     // scales took a fifth of its time: 32 rows' lanes are 32 passes of the L1.)
     uint32_t turns = 0;  // of 4 blocks, over all tiles
     bool ok = true;
-    Piece w;
-    for (int i = 0; ok && sched.get(i, KB, w); ++i) {
-      const int tile = w.tile;
+    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
       const Tile t = decode<BM>(bk, p, tile);
       const float* sa = p.a_scale + (static_cast<int64_t>(t.row0) + lane) * KB;
       const int64_t w_row = static_cast<int64_t>(t.e) * p.nsb;
@@ -313,7 +300,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
       const float* s0 = p.w_scale0 + (w_row + (GATED ? t.nb : 2 * t.nb)) * KB;
       const float* s1 = GATED ? p.w_scale1 + (w_row + t.nb) * KB
                               : p.w_scale0 + (w_row + min(2 * t.nb + 1, p.nsb - 1)) * KB;
-      for (int k0 = w.kb0; k0 < w.kb1; k0 += 4) {
+      for (int k0 = 0; k0 < KB; k0 += 4) {
         float4 a[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m)
@@ -350,18 +337,16 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
                         static_cast<uint32_t>(2 * half * HALF_N);
     uint8_t* stage_out = smem + STAGES * STAGE_BYTES + (warp - CTRL_WARPS) * OUT_STAGE;
     uint32_t fills = 0;  // bit s: parity of stage s's next fill
-    uint32_t turns = 0, xph = 0, jph = 0;
+    uint32_t turns = 0, xph = 0;
     bool ok = true;
-    Piece w;
-    for (int i = 0; ok && sched.get(i, KB, w); ++i) {
-      const int tile = w.tile;
+    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
       const Tile t = decode<BM>(bk, p, tile);
       const bool live = 32 * q < t.valid;  // the warp has bucket rows
       float2 acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
 #pragma unroll 1
-      for (int kb = w.kb0; kb < w.kb1; ++kb) {
+      for (int kb = 0; kb < KB; ++kb) {
         const int s = kb & (STAGES - 1), j = kb & 1;
         const uint32_t b = turns & 1u;
         if (s == 0 && !await(&sfull_bar[b], (turns >> 1) & 1u, 46, tile)) {
@@ -394,7 +379,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
         } else {
           arrive_if(&tempty_bar[half][j], first);
         }
-        if (s == STAGES - 1 || kb == w.kb1 - 1) {  // every lane has read the 4 blocks' scales
+        if (s == STAGES - 1 || kb == KB - 1) {  // every lane has read the 4 blocks' scales
           __syncwarp();
           arrive_if(&sfree_bar[b], first);
           ++turns;
@@ -402,114 +387,6 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
       }
       if (!ok) break;
       const int left = t.valid - 32 * q;  // rows of this warp, from its first
-      if (w.slot >= 0) {
-        // a piece: its sums go to the workspace; the CTA whose piece of the tile is the last to
-        // arrive there adds all of them up, first piece first
-        if (lane < left) {
-          float4* to = reinterpret_cast<float4*>(
-              p.partials + static_cast<int64_t>(w.slot) * SLOT_FLOATS + (half * BM + r) * HALF_N);
-#pragma unroll
-          for (int c = 0; c < 32; ++c)
-            __stcg(to + c, make_float4(acc[2 * c].x, acc[2 * c].y, acc[2 * c + 1].x,
-                                       acc[2 * c + 1].y));
-        }
-        const int cut = tile;
-        const int64_t tile0 = static_cast<int64_t>(cut) * sched.groups;
-        // its pieces' CTAs; each has the tile as its run's first, but for the first of them when
-        // that one's run starts in a tile before
-        const int c0 = sched.owner(tile0), c1 = sched.owner(tile0 + sched.groups - 1);
-        const bool starts = sched.begin(c0) == tile0;
-        __threadfence();
-        __syncwarp();
-        arrive_if(&join_bar[0], first);
-        if (warp == CTRL_WARPS) {
-          if (!await(&join_bar[0], jph, 47, tile)) break;
-          if (lane == 0) {
-            __threadfence();
-            const unsigned before = atomicAdd(p.arrivals + cut, 1u);
-            const int is_last = before == static_cast<unsigned>(c1 - c0);
-            if (is_last) p.arrivals[cut] = 0u;  // as the next launch wants it
-            __threadfence();
-            last_s = is_last;
-          }
-          __syncwarp();
-          arrive_if(&join_bar[1], first);
-        }
-        if (!await(&join_bar[1], jph, 48, tile)) break;
-        jph ^= 1u;
-        if (last_s != 0) {
-          __threadfence();
-          // A warp takes every second of its quarter's rows, 4 at a time, and a lane 4 columns
-          // of each half: a row's 1 KB is read at once, where a thread with a row to itself
-          // would wait for memory 32 times as often.
-#pragma unroll 1
-          for (int m0 = half; m0 < 32 && m0 < left; m0 += 8) {
-            float4 v[4][2];
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-              v[m][0] = v[m][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-            for (int c = c0; c <= c1; ++c) {
-              const int slot = 2 * c + (c == c0 && !starts ? 1 : 0);
-              const float4* from =
-                  reinterpret_cast<const float4*>(
-                      p.partials + static_cast<int64_t>(slot) * SLOT_FLOATS +
-                      (32 * q + m0) * HALF_N) + lane;
-#pragma unroll
-              for (int m = 0; m < 4; ++m)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                  if (m0 + 2 * m < left) {
-                    const float4 x = __ldcg(from + (h * BM + 2 * m) * HALF_N / 4);
-                    v[m][h].x += x.x;
-                    v[m][h].y += x.y;
-                    v[m][h].z += x.z;
-                    v[m][h].w += x.w;
-                  }
-            }
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              if (m0 + 2 * m >= left) break;
-              const int64_t row = static_cast<int64_t>(t.row0) + 32 * q + m0 + 2 * m;
-              if (GATED) {  // lanes 0-15 have 4 gate columns, lanes 16-31 the same of up
-                uint32_t most = 0;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  float* e = reinterpret_cast<float*>(&v[m][h]);
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    const float other = __shfl_xor_sync(0xffffffffu, e[k], 16);
-                    e[k] = silu_mul(lane < 16 ? e[k] : other, lane < 16 ? other : e[k]);
-                    most = max(most, __float_as_uint(e[k]) & 0x7FFFFFFFu);
-                  }
-                }
-                most = __reduce_max_sync(0xffffffffu, most);
-                const RowQuant rq(most);
-                if (lane < 16) {
-#pragma unroll
-                  for (int h = 0; h < 2; ++h) {
-                    const int col = t.nb * 128 + 64 * h + 4 * lane;
-                    if (col < p.N)
-                      *reinterpret_cast<uint32_t*>(p.h + row * p.N + col) =
-                          rq.pack(v[m][h].x, v[m][h].y, v[m][h].z, v[m][h].w);
-                  }
-                }
-                if (lane == 0) p.h_scale[row * p.nsb + t.nb] = rq.scale();
-              } else {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const int col = t.nb * BN + HALF_N * h + 4 * lane;
-                  if (col < p.N)
-                    *reinterpret_cast<uint2*>(p.out + row * p.N + col) =
-                        make_uint2(pack_bf16x2(v[m][h].x, v[m][h].y),
-                                   pack_bf16x2(v[m][h].z, v[m][h].w));
-                }
-              }
-            }
-          }
-        }
-        continue;
-      }
       if (GATED) {
         // h of this thread's 64 columns over its gate half of the accumulators, the row's
         // largest magnitude over both halves, then e4m3 and the scale
@@ -572,10 +449,10 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
 template <int MODE>
 cudaError_t launch(const CUtensorMap& a, const CUtensorMap& a32, const CUtensorMap& b0,
                    const CUtensorMap& b1, const Fp8Params& p, bool follows, cudaStream_t st) {
-  // at most one ragged row block per bucket, the rest full; each can be cut into pieces
+  // at most one ragged row block per bucket, the rest full
   const int64_t tiles = (p.rows / BM + (p.rows < p.E ? p.rows : p.E)) * p.n_blocks;
-  return launch_product(fp8_grouped_gemm_kernel<MODE>, tiles * ((p.kb + 3) / 4), THREADS,
-                        DYN_SMEM, follows, st, a, a32, b0, b1, p);
+  return launch_product(fp8_grouped_gemm_kernel<MODE>, tiles, THREADS, DYN_SMEM, follows, st, a,
+                        a32, b0, b1, p);
 }
 
 }  // namespace

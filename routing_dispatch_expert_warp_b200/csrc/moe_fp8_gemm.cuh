@@ -1,5 +1,5 @@
 // What the kernels of the 8-bit floating point products share: the parameters of a launch, the
-// table of buckets, the schedule of tiles over the CTAs, wrappers of single instructions, and
+// table of buckets, wrappers of single instructions, and
 // the tensor maps.  Included by those kernels' files only.
 #pragma once
 
@@ -45,7 +45,7 @@ constexpr int B_BYTES = BN * BK;
 
 enum Mode { FP8_LINEAR = 0, FP8_GATED = 1 };
 
-constexpr int SLOT_FLOATS = 2 * 128 * 128;
+constexpr int SLOT_FLOATS = 64 * BN;  // partial sums of a piece
 
 // Programmatic dependent launch: let the next launch's blocks start as this one's leave their
 // SMs; wait until the launch before has completed (at once when there is none to wait for).
@@ -184,64 +184,6 @@ __device__ void build_buckets(Buckets& t, const Fp8Params& p, int lane) {
   }
   if (lane == 0) t.tile_base[p.E] = carry * p.n_blocks;
 }
-
-// The work of one CTA: tiles, or pieces of tiles along the reduction.
-struct Piece {
-  int tile;
-  int kb0, kb1;  // its blocks of the reduction
-  int slot;      // -1: the whole tile; else where its partial sums go, 2 slots a CTA
-};
-
-struct Schedule {
-  int rounds;      // whole tiles this CTA takes: blockIdx.x + i * gridDim.x
-  int cut_tiles;   // all tiles, or none, are cut
-  int groups;      // groups of 4 blocks of a tile
-  int ctas;        // that share them
-  int64_t units;   // cut_tiles * groups
-
-  __device__ Schedule(int total, int KB) {
-    const int G = static_cast<int>(gridDim.x);
-    const int full = total / G, rest = total - full * G;
-    // Cut only when there are fewer than two whole rounds and the last would leave a tenth of
-    // the SMs' time unused.  (One token of the Mixtral-8x7B shaped layer, 224 and 32 tiles: 104
-    // us whole, 80 us cut.  With more rounds the SMs idle in the last one save power that the
-    // others use, and the joins cost more than they gain: 4096 x 4096 x 7168, 512 tiles: 129 us
-    // whole, 137 us cut.)
-    const bool cut = full < 2 && rest != 0 && (full + 1) * G * 10 > total * 11;
-    rounds = cut ? 0 : full + (static_cast<int>(blockIdx.x) < rest ? 1 : 0);
-    cut_tiles = cut ? total : 0;
-    groups = (KB + 3) >> 2;
-    units = static_cast<int64_t>(cut_tiles) * groups;
-    ctas = units < G ? static_cast<int>(units) : G;
-  }
-  // first unit of CTA c, and the CTA that has unit u
-  __device__ int64_t begin(int c) const { return units * c / ctas; }
-  __device__ int owner(int64_t u) const { return static_cast<int>(((u + 1) * ctas - 1) / units); }
-  // The i-th piece of this CTA (i counts up from 0); false past the last.
-  __device__ bool get(int i, int KB, Piece& w) const {
-    if (i < rounds) {
-      w.tile = static_cast<int>(blockIdx.x + static_cast<unsigned>(i) * gridDim.x);
-      w.kb0 = 0;
-      w.kb1 = KB;
-      w.slot = -1;
-      return true;
-    }
-    const int c = static_cast<int>(blockIdx.x);
-    if (c >= ctas) return false;
-    const int64_t u0 = begin(c), u1 = begin(c + 1);
-    const int first = static_cast<int>(u0 / groups);
-    const int t = first + i - rounds;
-    const int64_t t0 = static_cast<int64_t>(t) * groups;
-    if (t0 >= u1) return false;
-    const int g0 = t0 < u0 ? static_cast<int>(u0 - t0) : 0;
-    const int g1 = u1 - t0 < groups ? static_cast<int>(u1 - t0) : groups;
-    w.tile = t;
-    w.kb0 = 4 * g0;
-    w.kb1 = min(KB, 4 * g1);
-    w.slot = g0 == 0 && g1 == groups ? -1 : 2 * c + (t == first ? 0 : 1);
-    return true;
-  }
-};
 
 struct Tile {
   int e, nb, row0, valid;  // expert, column block, first row, rows from there in the bucket

@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_few_rows_kernel(
 
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);  // uniform
   const int lane = threadIdx.x & 31;
 
   if (warp == 0) {

@@ -168,15 +168,20 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
   // The whole warp waits for a barrier.  Once a wait has run out, here or elsewhere in the
   // block, every role's next wait fails and the roles unwind.
   auto await = [&](uint64_t* bar, uint32_t parity, unsigned site, int tile) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    const bool got = mbar_wait(bar, parity, p.wait_ns, &abort_s);
-    if (__all_sync(0xffffffffu, got)) return true;
-    if (lane == 0) {
-      if (!abort_s)
-        record_error(p.status, DEV_TIMEOUT, site, static_cast<unsigned long long>(tile));
-      abort_s = 1;
+    uint64_t since = 0;
+    while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+      const uint64_t now = global_ns();
+      if (since == 0) since = now;
+      if (__any_sync(0xffffffffu, abort_s != 0 || now - since > p.wait_ns)) {
+        if (lane == 0) {
+          if (!abort_s)
+            record_error(p.status, DEV_TIMEOUT, site, static_cast<unsigned long long>(tile));
+          abort_s = 1;
+        }
+        return false;
+      }
     }
-    return false;
+    return true;
   };
 
   if (warp == 0) {
@@ -256,7 +261,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
     uint32_t fills = 0, uses = 0;  // parities: stage s's next fill, accumulator j's next use
     bool ok = true, issued = false;
     for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-#pragma unroll 1
+#pragma unroll 4
       for (int kb = 0; kb < KB; ++kb) {
           const int s = kb & (STAGES - 1), j = kb & 1;
           if (!await(&full_bar[s], (fills >> s) & 1u, 42, tile) ||
@@ -345,7 +350,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
       float2 acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
-#pragma unroll 1
+#pragma unroll 2
       for (int kb = 0; kb < KB; ++kb) {
         const int s = kb & (STAGES - 1), j = kb & 1;
         const uint32_t b = turns & 1u;

@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_few_rows_kernel(
     // every fill must land before the block can exit
     for (int s = 0; s < STAGES; ++s)
       if ((armed >> s) & 1u)
-        mbar_wait(&full_bar[s], (armed_parity >> s) & 1u, p.wait_ns, nullptr);
+        mbar_wait(&full_bar[s], (armed_parity >> s) & 1u, kDrainNs, nullptr);
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_few_rows_kernel(
     }
     if (!ok && issued) {  // MMAs still reading smem / writing TMEM must finish first
       if (elect_one()) tc_commit(&drain_bar);
-      mbar_wait(&drain_bar, 0, p.wait_ns, nullptr);
+      mbar_wait(&drain_bar, 0, kDrainNs, nullptr);
       __syncwarp();
     }
   } else if (warp == 2) {

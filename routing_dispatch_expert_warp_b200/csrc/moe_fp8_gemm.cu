@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
     // every fill must land before the block can exit
     for (int s = 0; s < STAGES; ++s)
       if ((armed >> s) & 1u)
-        mbar_wait(&full_bar[s], (armed_parity >> s) & 1u, p.wait_ns, nullptr);
+        mbar_wait(&full_bar[s], (armed_parity >> s) & 1u, kDrainNs, nullptr);
     __syncwarp();
   } else if (warp < 3) {
     // ---------------------------------------------------------------- MMA issuers
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
     }
     if (!ok && issued) {  // MMAs still reading smem / writing TMEM must finish first
       if (elect_one()) tc_commit(&drain_bar[h]);
-      mbar_wait(&drain_bar[h], 0, p.wait_ns, nullptr);
+      mbar_wait(&drain_bar[h], 0, kDrainNs, nullptr);
       __syncwarp();
     }
   } else if (warp == 3) {

@@ -42,6 +42,9 @@ constexpr int BN = 256;      // weight rows of a tile
 constexpr int HALF_N = BN / 2;
 constexpr int STAGES = 4;
 constexpr int B_BYTES = BN * BK;
+// Limit of the waits for a block's own copies and MMAs before it exits, whatever the limit of
+// the others is: these end by themselves within microseconds.
+constexpr uint64_t kDrainNs = 1000000000ull;
 
 enum Mode { FP8_LINEAR = 0, FP8_GATED = 1 };
 

@@ -328,6 +328,126 @@ def test_grouped_gemm_reports_a_bucket_outside_the_rows():
     check_product(out, a_q, a_s, w_q, w_s, [0, 0, 0, 10], [10, 0, 0, 20])
 
 
+@pytest.mark.parametrize("seed", range(24))
+def test_grouped_gemm_random_buckets(seed):
+    """Random sizes and buckets, few rows and many; the workspace is used again and again, as the
+    pieces of cut tiles need it."""
+    g = np.random.default_rng(seed)
+    E = int(g.choice([1, 2, 5, 16, 64, 256]))
+    K, N = 16 * int(g.integers(1, 160)), 8 * int(g.integers(1, 200))
+    mean = float(g.choice([0.3, 3, 20, 100])) if E <= 16 else float(g.choice([0.3, 3]))
+    ws = M.alloc_fp8_workspace()
+    w_q, w_s = quantized_weights(torch.randn((E, N, K), generator=gen(seed)) / K ** 0.5)
+    for call in range(2):
+        counts = g.poisson(mean * g.exponential(1.0, E)).tolist()
+        counts[int(g.integers(E))] += 1
+        first, rows = starts(counts, int(g.integers(0, 3)))
+        a_q, a_s = quantized_rows(torch.randn((rows, K), generator=gen(seed + 50)).bfloat16())
+        out = torch.full((rows, N), 3.25, dtype=torch.bfloat16, device="cuda")
+        i32 = dict(dtype=torch.int32, device="cuda")
+        f, c = torch.tensor(first, **i32), torch.tensor(counts, **i32)
+        M.moe_fp8_grouped_gemm(a_q, a_s, f, c, w_q, w_s, out, ws)
+        M.moe_check_device_error(ws)
+        check_product(out, a_q, a_s, w_q, w_s, first, counts)
+        again = torch.full((rows, N), 3.25, dtype=torch.bfloat16, device="cuda")
+        M.moe_fp8_grouped_gemm(a_q, a_s, f, c, w_q, w_s, again, ws)
+        assert torch.equal(out, again)
+
+
+def test_grouped_gemm_buckets_in_any_order():
+    """Buckets need not lie in the experts' order, nor start where another ends."""
+    first, counts, rows, N, K = [90, 0, 40, 10], [9, 7, 33, 20], 100, 264, 400
+    a_q, a_s = quantized_rows(torch.randn((rows, K), generator=gen(1)))
+    w_q, w_s = quantized_weights(torch.randn((4, N, K), generator=gen(2)))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    out = torch.full((rows, N), 3.25, dtype=torch.bfloat16, device="cuda")
+    ws = M.alloc_fp8_workspace()
+    M.moe_fp8_grouped_gemm(a_q, a_s, torch.tensor(first, **i32), torch.tensor(counts, **i32),
+                           w_q, w_s, out, ws)
+    M.moe_check_device_error(ws)
+    check_product(out, a_q, a_s, w_q, w_s, first, counts)
+
+
+@pytest.mark.parametrize("E,rows,N", [(1, 600000, 4096), (256, 8000, 272000)],
+                         ids=["many rows", "few rows"])
+def test_grouped_gemm_offsets_beyond_32_bits(E, rows, N):
+    """The last rows' offsets in the output pass 2^31 elements, in either kernel."""
+    K, last = 16, slice(rows - 3, rows)
+    counts = [rows] if E == 1 else [0] * (E - 1) + [3]
+    first = [0] * (E - 1) + [rows - counts[-1]]
+    g = gen(4)
+    a_q, a_s = quantized_rows(torch.randn((1000, K), generator=g).repeat(rows // 1000, 1))
+    w = torch.zeros((E, N, K), device="cuda")
+    w[-1] = torch.randn((N, K), generator=g).cuda()
+    w_q, w_s = quantized_weights(w)
+    out = torch.full((rows, N), 3.25, dtype=torch.bfloat16, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ws = M.alloc_fp8_workspace()
+    M.moe_fp8_grouped_gemm(a_q, a_s, torch.tensor(first, **i32), torch.tensor(counts, **i32),
+                           w_q, w_s, out, ws)
+    M.moe_check_device_error(ws)
+    check_product(out[last], a_q[last], a_s[last], w_q[-1:], w_s[-1:], [0], [3])
+    assert E == 1 or (out[-4] == 3.25).all()
+
+
+def test_rows_offsets_beyond_32_bits():
+    rows, cols = 140000, 16384
+    x = torch.randn((7, cols), generator=gen(6)).bfloat16()
+    big = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+    big[-7:] = x.cuda()
+    q = torch.empty((rows, cols), dtype=E4M3, device="cuda")
+    s = torch.empty((rows, O.blocks(cols)), device="cuda")
+    M.moe_fp8_quantize_rows(big, q, s)
+    ref_q, ref_s = O.quantize_rows(x)
+    assert_same_scales(s[-7:], ref_s)
+    assert_same_codes(q[-7:], ref_q)
+    assert not q[:-7].view(torch.uint8)[::1000].any()
+
+
+def test_misaligned_tensors_are_refused():
+    x = torch.zeros((4, 256), device="cuda").bfloat16()
+    q = torch.zeros((4, 256), device="cuda").to(E4M3)
+    s = torch.zeros((9,), device="cuda")[1:].view(4, 2)
+    with pytest.raises(M.MoEError) as e:
+        M.moe_fp8_quantize_rows(x, q, s)
+    assert e.value.status == 1 and "aligned" in str(e.value)
+
+
+def test_nothing_is_written_outside_the_outputs():
+    """Every output inside a larger allocation whose other bytes hold a pattern."""
+    blocks = []
+
+    def inside(shape, dtype):
+        n = int(np.prod(shape)) * torch.empty((), dtype=dtype).element_size()
+        full = torch.full((1024 + n + 1024,), 0xA5, dtype=torch.uint8, device="cuda")
+        blocks.append((full, n))
+        return full[1024:1024 + n].view(dtype).view(shape)
+
+    for counts, d, f in (([1, 0, 37, 2], 272, 400), ([200, 3, 150], 400, 272)):
+        E, rows = len(counts), sum(counts)
+        first, _ = starts(counts)
+        i32 = dict(dtype=torch.int32, device="cuda")
+        cfg = M.make_config(rows, d, f, E, 1)
+        x = torch.randn((rows, d), generator=gen(1)).cuda().bfloat16()
+        x_q, x_s = inside((rows, d), E4M3), inside((rows, O.blocks(d)), torch.float32)
+        M.moe_fp8_permute_rows(cfg, x, torch.arange(rows, **i32).view(rows, 1), x_q, x_s)
+        parts = []
+        for shape in ((E, f, d), (E, f, d), (E, d, f)):
+            w = torch.randn(shape, generator=gen(2)).cuda()
+            parts += [inside(shape, E4M3), inside(M.fp8_scale_shape(shape), torch.float32)]
+            M.moe_fp8_quantize_weights(w, *parts[-2:])
+        h_q, h_s = inside((rows, f), E4M3), inside((rows, O.blocks(f)), torch.float32)
+        y = inside((rows, d), torch.bfloat16)
+        ws = inside((M.fp8_workspace_size(),), torch.uint8)
+        M.moe_fp8_workspace_init(ws)
+        M.moe_expert_ffn_fp8(cfg, x_q, x_s, torch.tensor(first, **i32),
+                             torch.tensor(counts, **i32), M.Fp8Experts(*parts), h_q, h_s, y, ws)
+        M.moe_check_device_error(ws)
+        check_product(y, h_q, h_s, parts[4], parts[5], first, counts)
+    for full, n in blocks:
+        assert (full[:1024] == 0xA5).all() and (full[1024 + n:] == 0xA5).all()
+
+
 # ------------------------------------------------------------------ FFN
 FFN = [  # counts, d, f
     ([1], 16, 16),
@@ -511,3 +631,31 @@ def test_layer_captured_into_a_graph():
         got = layer.bufs.out.clone()
         assert torch.equal(got, other(new))
     layer.check_device_error()
+
+
+@pytest.mark.parametrize("counts", [[1, 0, 2], [150, 0, 200]], ids=["few", "many"])
+def test_two_ffn_graphs_beside_each_other(counts):
+    """Two captured FFNs, each with a workspace of its own, replayed on two streams at once."""
+    d, f = 1520, 2064
+    runs = []
+    for seed in (1, 2):
+        args = list(make_ffn(counts, d, f, seed))
+        first = args.pop()
+        ws = M.alloc_fp8_workspace()
+        M.moe_expert_ffn_fp8(*args, ws)
+        want = args[8].clone()
+        graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            M.moe_expert_ffn_fp8(*args, ws, stream)
+        args[8].zero_()
+        runs.append((graph, stream, args, ws, want))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for graph, stream, *_ in runs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for graph, stream, args, ws, want in runs:
+        M.moe_check_device_error(ws)
+        assert torch.equal(args[8], want)

@@ -1057,14 +1057,15 @@ moe_status_t moe_fp8_grouped_gemm(int32_t E, int64_t rows, int64_t N, int64_t K,
   return run_fp8_gemm(name, g, ws, stream);
 }
 
-moe_status_t moe_expert_ffn_fp8(const moe_config_t* cfg, const void* x_q, const float* x_scale,
-                                const int32_t* expert_offsets, const int32_t* kept_counts,
-                                const moe_fp8_experts_t* w, void* h_q, float* h_scale,
-                                void* y_perm, void* ws, size_t ws_bytes, void* stream) {
-  const char* name = "moe_expert_ffn_fp8";
-  Shape s;
-  moe_status_t st = check_config(cfg, &s);
-  if (st != MOE_OK) return st;
+namespace {
+
+// What moe_expert_ffn_fp8 asks of its arguments.
+moe_status_t check_fp8_ffn(const char* name, const Shape& s, const void* x_q,
+                           const float* x_scale, const int32_t* expert_offsets,
+                           const int32_t* kept_counts, const moe_fp8_experts_t* w,
+                           const void* h_q, const float* h_scale, const void* y_perm,
+                           const void* ws, size_t ws_bytes) {
+  moe_status_t st;
   if (s.dtype != MOE_BF16)
     return fail(MOE_ERR_UNSUPPORTED, "%s: the layer's dtype must be bf16", name);
   if ((st = check_fp8_width(name, "d_model", s.d)) != MOE_OK) return st;
@@ -1081,6 +1082,22 @@ moe_status_t moe_expert_ffn_fp8(const moe_config_t* cfg, const void* x_q, const 
                   aligned16(w->w_up) && aligned16(w->up_scale) && aligned16(w->w_down) &&
                   aligned16(w->down_scale),
               "%s: tensors must be 16-byte aligned", name);
+  return MOE_OK;
+}
+
+}  // namespace
+
+moe_status_t moe_expert_ffn_fp8(const moe_config_t* cfg, const void* x_q, const float* x_scale,
+                                const int32_t* expert_offsets, const int32_t* kept_counts,
+                                const moe_fp8_experts_t* w, void* h_q, float* h_scale,
+                                void* y_perm, void* ws, size_t ws_bytes, void* stream) {
+  const char* name = "moe_expert_ffn_fp8";
+  Shape s;
+  moe_status_t st = check_config(cfg, &s);
+  if (st != MOE_OK) return st;
+  if ((st = check_fp8_ffn(name, s, x_q, x_scale, expert_offsets, kept_counts, w, h_q, h_scale,
+                          y_perm, ws, ws_bytes)) != MOE_OK)
+    return st;
   Fp8Gemm g{};
   g.E = s.E;
   g.rows = s.max_rows;
@@ -1120,17 +1137,15 @@ moe_status_t moe_layer_forward_fp8(const moe_config_t* cfg, const moe_layer_inpu
   const char* name = "moe_layer_forward_fp8";
   MOE_REQUIRE(in != nullptr && b != nullptr && f != nullptr,
               "%s: NULL inputs or buffers", name);
-  // what a later stage would refuse is refused before anything is enqueued
+  // what the stages on quantised rows would refuse is refused before anything is enqueued
   Shape s;
   moe_status_t st = check_config(cfg, &s);
   if (st != MOE_OK) return st;
-  if (s.dtype != MOE_BF16)
-    return fail(MOE_ERR_UNSUPPORTED, "%s: the layer's dtype must be bf16", name);
-  if ((st = check_fp8_width(name, "d_model", s.d)) != MOE_OK) return st;
-  if ((st = check_fp8_width(name, "d_ff", s.f)) != MOE_OK) return st;
-  if ((st = check_fp8_ws(name, fp8_ws, fp8_ws_bytes)) != MOE_OK) return st;
-  MOE_REQUIRE(f->x_q && f->x_scale && f->h_q && f->h_scale && experts && b->y_perm && b->out,
-              "%s: NULL pointer", name);
+  if ((st = check_fp8_ffn(name, s, f->x_q, f->x_scale, b->expert_offsets, b->kept_counts, experts,
+                          f->h_q, f->h_scale, b->y_perm, fp8_ws, fp8_ws_bytes)) != MOE_OK)
+    return st;
+  MOE_REQUIRE(b->assign_row && b->out, "%s: NULL pointer", name);
+  MOE_REQUIRE(aligned16(b->assign_row), "%s: tensors must be 16-byte aligned", name);
   st = moe_route_ex(cfg, in->x, in->w_router, in->w_router_split, in->logit_bias,
                     in->bias_row_stride, b->logits, b->topk_idx, b->topk_w, ws, ws_bytes, stream);
   if (st != MOE_OK) return st;

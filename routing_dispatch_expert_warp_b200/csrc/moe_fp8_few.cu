@@ -3,9 +3,9 @@
 // rows twice over (two halves), the bucket rows its N = 16 .. 64 columns, taken in steps of 16.
 // What bounds such a product is reading each expert's weight once.  With the rows in the MMA's
 // 128 places, 4 rows cost the tensor cores and the epilogue as much as 128 (and power, which
-// the clocks pay for: a DeepSeek-shaped decode step of 4 rows an expert took 2.08 ms there, and
-// takes what the table of the design notes says here); with the weight in them, a block of 128
-// costs the epilogue 16 sums a thread.
+// the clocks pay for): a DeepSeek-shaped decode step of 4 rows an expert takes 2.08 ms there and
+// 1.66 here, which is the time of reading the weights.  Here a block of 128 costs the epilogue 16
+// sums a thread.
 //
 // FP8_LINEAR: the halves are 128 output columns each.  FP8_GATED: 128 rows of W_gate and the
 // same 128 of W_up; a thread has one column of h, and a tile's 128 columns are one block of h's

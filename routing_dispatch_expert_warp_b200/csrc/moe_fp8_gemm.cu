@@ -19,8 +19,7 @@
 // Block = 12 warps, one block per SM, persistent over tiles (numbered expert by expert,
 // column block by column block, row blocks innermost, so that blocks running at the same time
 // share weight tiles through L2; the table of tiles is built on the device).  Every tile starts
-// at stage 0 of the ring of 4 and at accumulator 0; each barrier's parity is a bit of a mask.  (The loops over the
-// reduction are not unrolled: four copies of the epilogue's missed the instruction cache.)
+// at stage 0 of the ring of 4 and at accumulator 0; each barrier's parity is a bit of a mask.
 //   warp 0             TMA producer: 128 x 128 bytes of rows, 256 x 128 of weights, 128-byte
 //                      swizzle.  Of a bucket's last rows only as many groups of 32 as hold rows
 //                      are loaded.
@@ -34,7 +33,16 @@
 //                      bucket rows only keeps step.
 // A hand-over between an MMA issuer and an epilogue takes some 200 cycles each way.  With the
 // halves apart, four accumulators of 128 columns are on their way round instead of two of 256,
-// and one half's epilogue computes while the other's waits.
+// and one half's epilogue computes while the other's waits.  (One issuer with MMAs of 256
+// columns for both halves: 115 us for 4096 x 4096 x 7168 and 1.44 ms for the Mixtral-8x7B
+// shaped prefill, against 116.5 and 1.45 here; but 8.1 ms for the DeepSeek-shaped prefill of
+// 16384 tokens against 7.6, and 16.4 us for 13 ragged buckets against 15.6.)
+// What bounds it: the outer sum.  The epilogue adds every block's 128 x 256 partial sums up in
+// fp32 on the general cores, and the card's power limit holds the clock at 1.45 to 1.65 GHz
+// meanwhile: 1.9 to 2.06 PFLOP/s.  Without the epilogue's sums the copies and MMAs run at some
+// 2.5, without the MMAs the sums do as well.  Each instruction of the epilogue's loop counts:
+// its own loads of scales cost a fifth, a warp number that is not known to be uniform 5 to 9%,
+// and four copies of the loop instead of two missed the instruction cache.
 // (Tiles are not cut along the reduction when they are fewer than the SMs: a cut tile's 128 KB
 // of partial sums and their join take as long as 60 to 75 of its blocks.  256 x 4096 x 14336, 32
 // tiles: 60 us whole, 55 cut; 384 x 7168 x 2048: 17 us whole, 41 cut.)
@@ -45,7 +53,10 @@ namespace moe {
 namespace {
 
 constexpr int BM = 128;
-constexpr int kFewRows = 32;  // mean rows of a bucket up to which moe_fp8_few.cu takes them
+// Mean rows of a bucket up to which moe_fp8_few.cu takes them.  The FFN of 8 experts of 4096 x
+// 14336, few-rows kernel against this one: 32 rows a bucket 248 us against 257, 48 rows 260
+// against 261, 64 rows 329 against 266.
+constexpr int kFewRows = 32;
 constexpr int A_BYTES = BM * BK;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int CTRL_WARPS = 4;
@@ -263,25 +274,25 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
     for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
 #pragma unroll 4
       for (int kb = 0; kb < KB; ++kb) {
-          const int s = kb & (STAGES - 1), j = kb & 1;
-          if (!await(&full_bar[s], (fills >> s) & 1u, 42, tile) ||
-              !await(&tempty_bar[h][j], ((uses >> j) & 1u) ^ 1u, 42, tile)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          if (elect_one()) {
-            const uint32_t d_tmem = tmem_base + static_cast<uint32_t>((2 * h + j) * HALF_N);
+        const int s = kb & (STAGES - 1), j = kb & 1;
+        if (!await(&full_bar[s], (fills >> s) & 1u, 42, tile) ||
+            !await(&tempty_bar[h][j], ((uses >> j) & 1u) ^ 1u, 42, tile)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t d_tmem = tmem_base + static_cast<uint32_t>((2 * h + j) * HALF_N);
 #pragma unroll
-            for (int kk = 0; kk < BK / 32; ++kk)  // descriptors count 16-byte units
-              tc_mma_e4m3(d_tmem, a_desc + (s * STAGE_BYTES + kk * 32) / 16,
-                          b_desc + (s * STAGE_BYTES + kk * 32) / 16, idesc, kk != 0 ? 1u : 0u);
-            tc_commit(&done_bar[h][s]);
-          }
-          __syncwarp();
-          issued = true;
-          fills ^= 1u << s;
-          uses ^= 1u << j;
+          for (int kk = 0; kk < BK / 32; ++kk)  // descriptors count 16-byte units
+            tc_mma_e4m3(d_tmem, a_desc + (s * STAGE_BYTES + kk * 32) / 16,
+                        b_desc + (s * STAGE_BYTES + kk * 32) / 16, idesc, kk != 0 ? 1u : 0u);
+          tc_commit(&done_bar[h][s]);
+        }
+        __syncwarp();
+        issued = true;
+        fills ^= 1u << s;
+        uses ^= 1u << j;
       }
     }
     if (!ok && issued) {  // MMAs still reading smem / writing TMEM must finish first
@@ -422,8 +433,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
           store_rows64(stage_out, w, p.h + (static_cast<int64_t>(t.row0) + 32 * q) * p.N + col,
                        p.N, left, p.N - col, lane);
           if (half == 0 && lane < left)
-            p.h_scale[(static_cast<int64_t>(t.row0) + r) * p.nsb + t.nb] =
-                rq.scale();
+            p.h_scale[(static_cast<int64_t>(t.row0) + r) * p.nsb + t.nb] = rq.scale();
         }
       } else if (live) {
         const int col = t.nb * BN + HALF_N * half;
@@ -433,9 +443,8 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
         for (int c = 0; c < 4; ++c) {
           uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
+          for (int i = 0; i < 16; ++i)
             w[i] = pack_bf16x2(acc[16 * c + i].x, acc[16 * c + i].y);
-          }
           store_rows64(stage_out, w, to + 64 * c, static_cast<int64_t>(p.N) * 2, left,
                        2 * (p.N - col - 32 * c), lane);
         }
@@ -494,7 +503,6 @@ cudaError_t launch_fp8_gemm(const Fp8Gemm& g, void* ws, uint64_t wait_ns, cudaSt
   p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kFp8PartialsOffset);
   p.status = static_cast<DevStatus*>(ws);
   p.wait_ns = wait_ns;
-  // Few rows an expert: the kernel that gives the weight the MMA's 128 places.
   if (g.rows <= kFewRows * static_cast<int64_t>(g.E)) return launch_fp8_few_rows(g, p, st, why);
   CUtensorMap a, a32, b0, b1;
   if (!map_rows(&a, g.a, g.rows, g.K, BM) || !map_rows(&a32, g.a, g.rows, g.K, 32) ||

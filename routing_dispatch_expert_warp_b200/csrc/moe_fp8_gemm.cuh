@@ -1,6 +1,6 @@
 // What the kernels of the 8-bit floating point products share: the parameters of a launch, the
-// table of buckets, wrappers of single instructions, and
-// the tensor maps.  Included by those kernels' files only.
+// table of buckets, wrappers of single instructions, and the tensor maps.  Included by those
+// kernels' files only.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -92,7 +92,8 @@ __device__ __forceinline__ void arrive_if(uint64_t* bar, uint32_t who) {
 // 4 scales from block kb on (0 past the last of n).
 __device__ __forceinline__ float4 scales4(const float* s, int kb, int n) {
   if ((n & 3) == 0)
-    return kb < n ? __ldg(reinterpret_cast<const float4*>(s + kb)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    return kb < n ? __ldg(reinterpret_cast<const float4*>(s + kb))
+                  : make_float4(0.f, 0.f, 0.f, 0.f);
   return make_float4(kb < n ? __ldg(s + kb) : 0.f, kb + 1 < n ? __ldg(s + kb + 1) : 0.f,
                      kb + 2 < n ? __ldg(s + kb + 2) : 0.f, kb + 3 < n ? __ldg(s + kb + 3) : 0.f);
 }
@@ -103,7 +104,11 @@ __device__ __forceinline__ float pick(const float4& v, int i) {
 // One lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
   return p != 0;
 }
 __device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
@@ -160,7 +165,7 @@ struct Buckets {
 // By one whole warp: every bucket cut to the rows there are, and the tiles before each.
 template <int ROWS>  // of a tile
 __device__ void build_buckets(Buckets& t, const Fp8Params& p, int lane) {
-  int carry = 0;
+  int64_t carry = 0;
   for (int e0 = 0; e0 < p.E; e0 += 32) {
     const int e = e0 + lane;
     int mb = 0;
@@ -182,10 +187,14 @@ __device__ void build_buckets(Buckets& t, const Fp8Params& p, int lane) {
       const int o = __shfl_up_sync(0xffffffffu, v, off);
       if (lane >= off) v += o;
     }
-    if (e < p.E) t.tile_base[e] = (carry + v - mb) * p.n_blocks;
+    if (e < p.E) t.tile_base[e] = static_cast<int>(carry + v - mb) * p.n_blocks;
     carry += __shfl_sync(0xffffffffu, v, 31);
   }
-  if (lane == 0) t.tile_base[p.E] = carry * p.n_blocks;
+  // (only buckets that overlap can have more tiles than an int counts: then none is taken)
+  const bool fits = carry * p.n_blocks <= 2147483647;
+  if (!fits && blockIdx.x == 0)
+    record_error(p.status, DEV_BAD_BUCKET, 40, static_cast<unsigned long long>(p.E - 1));
+  if (lane == 0) t.tile_base[p.E] = fits ? static_cast<int>(carry) * p.n_blocks : 0;
 }
 
 struct Tile {
@@ -213,7 +222,7 @@ __device__ __forceinline__ Tile decode(const Buckets& t, const Fp8Params& p, int
 
 // ------------------------------------------------------------------ tensor maps
 inline bool encode(CUtensorMap* m, int rank, const void* base, const cuuint64_t* dims,
-            const cuuint64_t* strides, const cuuint32_t* box) {
+                   const cuuint64_t* strides, const cuuint32_t* box) {
   const cuuint32_t estr[3] = {1, 1, 1};
   return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<cuuint32_t>(rank),
                               const_cast<void*>(base), dims, strides, box, estr,
@@ -232,14 +241,13 @@ inline bool map_rows(CUtensorMap* m, const void* base, int64_t rows, int64_t K, 
 
 // [E, N, K] bytes, boxes of 1 x box_n x 128
 inline bool map_weights(CUtensorMap* m, const void* base, int64_t E, int64_t N, int64_t K,
-                 uint32_t box_n) {
+                        uint32_t box_n) {
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(N),
                               static_cast<cuuint64_t>(E)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(N * K)};
   const cuuint32_t box[3] = {BK, box_n, 1};
   return encode(m, 3, base, dims, strides, box);
 }
-
 
 // One launch of at most one block per SM and `most` blocks; `follows`: see Fp8Gemm.
 template <typename... Params, typename... Args>

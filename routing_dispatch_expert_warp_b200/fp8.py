@@ -14,8 +14,8 @@ from typing import Optional
 
 import torch
 
-from . import _abi
-from ._abi import (MoeConfig, MoeFp8Buffers, MoeFp8Experts, MoeLayerInputs, check)
+from . import LayerBuffers, MoELayer, _abi, alloc_workspace
+from ._abi import MoeConfig, MoeFp8Buffers, MoeFp8Experts, MoeLayerInputs, check
 
 E4M3 = torch.float8_e4m3fn
 _CODE = {torch.float32: 0, torch.bfloat16: 1}  # moe_dtype_t
@@ -85,6 +85,14 @@ def _call(fn, device: torch.device, stream, *args) -> None:
         check(status)
 
 
+def _allocating_on(stream):
+    """New tensors' memory comes from work that `stream` has already been given (another
+    stream's may still be in use there when `stream` writes to it)."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return torch.cuda.stream(stream)
+    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream)))
+
+
 def _max_rows(cfg: MoeConfig) -> int:
     r = _abi.lib().moe_max_rows(ctypes.byref(cfg))
     if r < 0:
@@ -136,7 +144,9 @@ def fp8_workspace_size(device="cuda") -> int:
 def alloc_fp8_workspace(device="cuda", stream=None) -> torch.Tensor:
     """A workspace, initialised.  Calls on one workspace must not overlap: one for each stream,
     and for each captured graph that may run beside another."""
-    ws = torch.empty(fp8_workspace_size(device), dtype=torch.uint8, device=device)
+    n = fp8_workspace_size(device)
+    with _allocating_on(stream):
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
     moe_fp8_workspace_init(ws, stream)
     return ws
 
@@ -208,8 +218,9 @@ class Fp8Experts:
         """Quantise a layer's fp32 or bf16 weights."""
         parts = []
         for w in (w_gate, w_up, w_down):
-            q = torch.empty(w.shape, dtype=E4M3, device=w.device)
-            s = torch.empty(fp8_scale_shape(w.shape), dtype=torch.float32, device=w.device)
+            with _allocating_on(stream):
+                q = torch.empty(w.shape, dtype=E4M3, device=w.device)
+                s = torch.empty(fp8_scale_shape(w.shape), dtype=torch.float32, device=w.device)
             moe_fp8_quantize_weights(w, q, s, stream)
             parts += [q, s]
         return Fp8Experts(*parts)
@@ -244,7 +255,7 @@ def moe_expert_ffn_fp8(cfg, x_q, x_scale, expert_offsets, kept_counts, experts: 
 class Fp8LayerBuffers:
     """Every output and intermediate of one layer forward: the layer's own (without x_perm and
     h) and the quantised rows."""
-    layer: "LayerBuffers"  # noqa: F821
+    layer: LayerBuffers
     x_q: torch.Tensor
     x_scale: torch.Tensor
     h_q: torch.Tensor
@@ -252,7 +263,6 @@ class Fp8LayerBuffers:
 
     @staticmethod
     def allocate(cfg: MoeConfig, device="cuda") -> "Fp8LayerBuffers":
-        from . import LayerBuffers
         R = max(_max_rows(cfg), 1)
         layer = LayerBuffers.allocate(cfg, device, gather=True, hidden=False)
 
@@ -280,22 +290,27 @@ def moe_layer_forward_fp8(cfg, inputs: MoeLayerInputs, experts: Fp8Experts, bufs
           wn)
 
 
-class MoELayerFp8:
+class MoELayerFp8(MoELayer):
     """MoELayer with its experts in 8-bit floating point: the same routing, dispatch, combine
-    and statistics (bf16 layers).  forward(x) enqueues the whole layer and returns the output,
-    a view of the layer's own buffer that the next call overwrites."""
+    and statistics (bf16 layers), on the experts' device.  forward(x) enqueues the whole layer
+    and returns the output, a view of the layer's own buffer that the next call overwrites."""
 
-    def __init__(self, cfg: MoeConfig, w_router, experts: Fp8Experts, logit_bias=None,
-                 device="cuda"):
-        from . import alloc_workspace, router_split
+    def __init__(self, cfg: MoeConfig, w_router, experts: Fp8Experts, logit_bias=None):
         _fits(cfg, experts)
+        dev = experts.w_gate.device
+        _need(w_router, "w_router", torch.float32, (cfg.d_model, cfg.E), dev)
+        if logit_bias is not None:
+            one = logit_bias.dim() == 1
+            _need(logit_bias, "logit_bias", torch.float32,
+                  (cfg.E,) if one else (cfg.T, max(cfg.E, logit_bias.shape[-1])), dev)
         self.cfg, self.w_router, self.experts, self.logit_bias = cfg, w_router, experts, logit_bias
-        self.ws = alloc_workspace(cfg, device)
-        self.fp8_ws = alloc_fp8_workspace(device)
-        self.fp8_bufs = Fp8LayerBuffers.allocate(cfg, device)
-        self.bufs = self.fp8_bufs.layer
-        self._structs = self.bufs.as_struct(True), self.fp8_bufs.as_struct()
-        self.w_router_split = router_split(cfg, w_router)
+        with torch.cuda.device(dev):
+            self.ws = alloc_workspace(cfg, dev)
+            self.fp8_ws = alloc_fp8_workspace(dev)
+            self.fp8_bufs = Fp8LayerBuffers.allocate(cfg, dev)
+            self.bufs = self.fp8_bufs.layer
+            self._structs = self.bufs.as_struct(True), self.fp8_bufs.as_struct()
+            self.resplit_router()
 
     def inputs(self, x) -> MoeLayerInputs:
         b, split = self.logit_bias, self.w_router_split
@@ -316,5 +331,11 @@ class MoELayerFp8:
 
     def check_device_error(self, stream: Optional[torch.cuda.Stream] = None) -> None:
         """Report (MoEError) and clear the kernel-side errors of the forwards so far."""
-        for ws in (self.ws, self.fp8_ws):
-            _call(_abi.lib().moe_check_device_error, ws.device, stream, ws.data_ptr(), ws.numel())
+        check_error = _abi.lib().moe_check_device_error
+        _call(check_error, self.ws.device, stream, self.ws.data_ptr(), self.ws.numel())
+        try:
+            _call(check_error, self.ws.device, stream, self.fp8_ws.data_ptr(),
+                  self.fp8_ws.numel())
+        except _abi.MoEError:
+            moe_fp8_workspace_init(self.fp8_ws, stream)  # (a run-out wait leaves counters behind)
+            raise

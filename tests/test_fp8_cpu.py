@@ -145,6 +145,41 @@ def test_layer_refuses(lib):
     assert call(cfg=M.make_config(4, 128, 256, 8, 2, dtype=M.F32)) == UNSUPPORTED
 
 
+def test_layer_refuses_before_it_enqueues(lib):
+    """What the expert stages would refuse is refused before the router runs: here, where no
+    kernel can run, the refusal and not the failed launch is what comes back."""
+    n = ws_bytes(lib)
+    cfg = M.make_config(4, 128, 256, 8, 2)
+    inp = _abi.MoeLayerInputs()
+    inp.x = inp.w_router = P
+    buf = _abi.MoeLayerBuffers()
+    for f, _ in _abi.MoeLayerBuffers._fields_:
+        setattr(buf, f, P)
+    for e, fb in ((experts_struct(up_scale=None), (P, P, P, P)),
+                  (experts_struct(w_down=P + 8), (P, P, P, P)),
+                  (experts_struct(), (P + 4, P, P, P)),
+                  (experts_struct(), (P, P, P, P + 8))):
+        f = _abi.MoeFp8Buffers(*fb)
+        assert lib.moe_layer_forward_fp8(ctypes.byref(cfg), ctypes.byref(inp), ctypes.byref(e),
+                                         ctypes.byref(buf), ctypes.byref(f), P,
+                                         M.workspace_size(cfg), P, n, None) == INVALID
+        assert b"moe_layer_forward_fp8" in lib.moe_last_error()
+
+
+def test_layer_class_refuses_what_does_not_fit(lib):
+    E, d, f = 4, 64, 48
+    q = lambda *s: torch.zeros(s, dtype=M.fp8.E4M3)  # noqa: E731
+    z = lambda *s: torch.zeros(M.fp8_scale_shape(s))  # noqa: E731
+    ex = M.Fp8Experts(q(E, f, d), z(E, f, d), q(E, f, d), z(E, f, d), q(E, d, f), z(E, d, f))
+    cfg = M.make_config(4, d, f, E, 1)
+    w = torch.zeros(d, E)
+    for router, bias in ((w.bfloat16(), None), (w.t().contiguous(), None), (w[:, ::2], None),
+                         (w, torch.zeros(E + 1)), (w, torch.zeros(3, E)), (w, torch.zeros(4, 2)),
+                         (w, torch.zeros(E, dtype=torch.float64)), (w.to("meta"), None)):
+        with pytest.raises(ValueError):
+            M.MoELayerFp8(cfg, router, ex, bias)
+
+
 def test_struct_layout_matches_header(tmp_path):
     src = tmp_path / "layout.c"
     src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "moe.h"\nint main(void) {\n'

@@ -633,6 +633,75 @@ def test_layer_captured_into_a_graph():
     layer.check_device_error()
 
 
+def test_layer_is_a_layer():
+    """What MoELayer offers beside forward: a router weight changed in place, the counters of
+    second choices, a captured forward."""
+    shape = W.reduced(W.DSV3_DECODE, 64, 256, 128)
+    inp = W.make_inputs(shape, device="cuda")
+    cfg = M.config_from_shape(shape)
+    experts = M.Fp8Experts.quantize(inp.w_gate, inp.w_up, inp.w_down)
+    w_router = inp.w_router.clone()
+    layer = M.MoELayerFp8(cfg, w_router, experts, inp.logit_bias)
+    layer(inp.x)
+    w_router.copy_(inp.w_router.flip(1))
+    layer.resplit_router()
+    out = layer(inp.x).clone()
+    fresh = M.MoELayerFp8(cfg, w_router, experts, inp.logit_bias)
+    assert torch.equal(out, fresh(inp.x))
+    routed, kept, _ = layer.pick_rank_counts()
+    assert torch.equal(routed.sum(0), layer.bufs.routed_counts)
+    assert torch.equal(kept.sum(0), layer.bufs.kept_counts)
+    x = inp.x.clone()
+    graph = layer.capture(x)
+    x.copy_(inp.x.flip(0))
+    graph.replay()
+    assert torch.equal(layer.bufs.out, fresh(inp.x.flip(0).contiguous()))
+    layer.check_device_error()
+
+
+def test_weights_and_workspace_on_another_stream():
+    """Quantised and initialised on a side stream that runs late, into memory that the current
+    stream has just let go of while still writing to it."""
+    w = torch.randn(3, 256, 512, device="cuda", dtype=torch.bfloat16)
+    want = M.Fp8Experts.quantize(w, w, w.transpose(1, 2).contiguous())
+    wd = w.transpose(1, 2).contiguous()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for handle in (side, side.cuda_stream):
+        junk = [torch.empty(w.shape, dtype=M.fp8.E4M3, device="cuda") for _ in range(6)]
+        torch.cuda._sleep(20_000_000)
+        for t in junk:
+            t.view(torch.uint8).fill_(0x5A)
+        del junk, t
+        got = M.Fp8Experts.quantize(w, w, wd, handle)
+        ws = M.alloc_fp8_workspace(stream=handle)
+        torch.cuda.synchronize()
+        for name in ("w_gate", "w_up", "w_down"):
+            assert np.array_equal(codes(getattr(got, name)), codes(getattr(want, name))), name
+        assert not ws[:4096].any()
+
+
+def test_check_after_a_wait_ran_out_restores_the_workspace():
+    """A launch that gave up leaves arrival counters behind; the layer's check reports it and
+    leaves a workspace that the next forward can use."""
+    shape = W.reduced(W.MIXTRAL_8X7B, 1, 1024, 512)
+    inp = W.make_inputs(shape, device="cuda")
+    cfg = M.config_from_shape(shape)
+    experts = M.Fp8Experts.quantize(inp.w_gate, inp.w_up, inp.w_down)
+    layer = M.MoELayerFp8(cfg, inp.w_router, experts, inp.logit_bias)
+    want = layer(inp.x).clone()
+    layer.check_device_error()
+    words = layer.fp8_ws[:4096].view(torch.int32)
+    assert not words.any()
+    words[64:128] = 1  # counters of cut tiles
+    words[0] = 1       # a status: some wait ran out
+    with pytest.raises(M.MoEError):
+        layer.check_device_error()
+    assert not words.any()
+    assert torch.equal(layer(inp.x), want)
+    layer.check_device_error()
+
+
 @pytest.mark.parametrize("counts", [[1, 0, 2], [150, 0, 200]], ids=["few", "many"])
 def test_two_ffn_graphs_beside_each_other(counts):
     """Two captured FFNs, each with a workspace of its own, replayed on two streams at once."""

@@ -9,6 +9,7 @@ enqueued.  The calls run on the tensors' device, on `stream` (None: its current 
 from __future__ import annotations
 
 import ctypes
+import functools
 from dataclasses import dataclass, field
 from typing import Optional
 
@@ -61,6 +62,7 @@ def _source(t, name: str, axes: int) -> int:
 # as long as a launch.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _call(fn, device: torch.device, stream, *args) -> None:
@@ -76,7 +78,7 @@ def _call(fn, device: torch.device, stream, *args) -> None:
         raw = stream.cuda_stream
     else:
         raw = int(stream)
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         status = fn(*args, raw)
     else:
         with torch.cuda.device(index):
@@ -94,7 +96,12 @@ def _allocating_on(stream):
 
 
 def _max_rows(cfg: MoeConfig) -> int:
-    r = _abi.lib().moe_max_rows(ctypes.byref(cfg))
+    return _max_rows_of(bytes(cfg))
+
+
+@functools.lru_cache(maxsize=256)  # a function of the configuration's values; 1 us to ask for
+def _max_rows_of(values: bytes) -> int:
+    r = _abi.lib().moe_max_rows(ctypes.byref(MoeConfig.from_buffer_copy(values)))
     if r < 0:
         raise _abi.MoEError(1, _abi.lib().moe_last_error().decode())
     return r

@@ -47,29 +47,26 @@ struct Piece {
 
 struct Schedule {
   int rounds;      // whole tiles this CTA takes: blockIdx.x + i * gridDim.x
-  int cut_tiles;   // all tiles, or none, are cut
-  int groups;      // groups of 4 blocks of a tile
-  int ctas;        // that share them
-  int64_t units;   // cut_tiles * groups
+  int ctas;        // that share the blocks of all tiles, when tiles are cut (else 0)
+  int64_t units;   // those blocks: total * KB
 
   __device__ Schedule(int total, int KB) {
     const int G = static_cast<int>(gridDim.x);
     const int full = total / G, rest = total - full * G;
     // Cutting saves the blocks of the reduction that the last round leaves unused and costs a
-    // join, as long as some 14 of a tile's blocks.  (One row, N = 4096, K = 4096, 16 tiles, 28
-    // blocks saved: 19.1 us whole, 11.7 cut.  16 rows, 7168, 2048, 13 saved: 12.9 and 13.0.  8
-    // experts' rows, 7168, 2048, 8 saved: 29.2 and 32.0.)
-    constexpr int join_blocks = 14;
+    // join; and the tiles of a last round that is half full share the memory's whole rate
+    // anyway.  (Two experts' rows, K = 4096, N = 28672, 16 blocks saved: 44.1 us whole, 45.1 cut;
+    // N = 8192, 18 saved: 20.9 and 21.5; N = 4096, 25 saved: 18.8 and 16.6; N = 20480, 29 saved:
+    // 42.0 and 35.6.)
+    constexpr int join_blocks = 20;
     const bool cut = full < 2 && rest != 0 &&
                      static_cast<int64_t>((full + 1) * G - total) * KB >
                          static_cast<int64_t>(join_blocks) * G;
     rounds = cut ? 0 : full + (static_cast<int>(blockIdx.x) < rest ? 1 : 0);
-    cut_tiles = cut ? total : 0;
-    groups = (KB + 3) >> 2;
-    units = static_cast<int64_t>(cut_tiles) * groups;
-    ctas = units < G ? static_cast<int>(units) : G;
+    units = cut ? static_cast<int64_t>(total) * KB : 0;
+    ctas = units < 4 * G ? static_cast<int>((units + 3) >> 2) : G;
   }
-  // first unit of CTA c, and the CTA that has unit u
+  // first block of CTA c, and the CTA that has block u
   __device__ int64_t begin(int c) const { return units * c / ctas; }
   __device__ int owner(int64_t u) const { return static_cast<int>(((u + 1) * ctas - 1) / units); }
   // The i-th piece of this CTA (i counts up from 0); false past the last.
@@ -84,19 +81,26 @@ struct Schedule {
     const int c = static_cast<int>(blockIdx.x);
     if (c >= ctas) return false;
     const int64_t u0 = begin(c), u1 = begin(c + 1);
-    const int first = static_cast<int>(u0 / groups);
+    const int first = static_cast<int>(u0 / KB);
     const int t = first + i - rounds;
-    const int64_t t0 = static_cast<int64_t>(t) * groups;
+    const int64_t t0 = static_cast<int64_t>(t) * KB;
     if (t0 >= u1) return false;
-    const int g0 = t0 < u0 ? static_cast<int>(u0 - t0) : 0;
-    const int g1 = u1 - t0 < groups ? static_cast<int>(u1 - t0) : groups;
     w.tile = t;
-    w.kb0 = 4 * g0;
-    w.kb1 = min(KB, 4 * g1);
-    w.slot = g0 == 0 && g1 == groups ? -1 : 2 * c + (t == first ? 0 : 1);
+    w.kb0 = t0 < u0 ? static_cast<int>(u0 - t0) : 0;
+    w.kb1 = u1 - t0 < KB ? static_cast<int>(u1 - t0) : KB;
+    w.slot = w.kb0 == 0 && w.kb1 == KB ? -1 : 2 * c + (t == first ? 0 : 1);
     return true;
   }
 };
+
+__device__ __forceinline__ unsigned add_acq_rel(unsigned* at, unsigned v) {
+  unsigned before;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;"
+               : "=r"(before)
+               : "l"(at), "r"(v)
+               : "memory");
+  return before;
+}
 
 // One bucket row of a tile: the lane's sums of weight rows 4 lane .. + 3 of either half.
 template <int MODE>
@@ -152,12 +156,13 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_few_rows_kernel(
   const int lane = threadIdx.x & 31;
 
   if (warp == 0) {
-    build_buckets<TM>(bk, p, lane);
     if (lane == 0) {
       prefetch_tensormap(&tm_a);
       prefetch_tensormap(&tm_b0);
       if (GATED) prefetch_tensormap(&tm_b1);
     }
+    if (!p.follows) wait_for_previous();
+    build_buckets<TM>(bk, p, lane);
   } else if (warp == 1) {
     tmem_alloc(&tmem_base_s, TMEM_COLS);
     tmem_relinquish();
@@ -209,12 +214,12 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_few_rows_kernel(
     uint32_t armed = 0, armed_parity = 0;
     bool ok = true, waited = false;
     int early = 0;  // blocks of the first piece whose weights were loaded ahead
+    int s = 0;      // the next block's stage
     Piece w;
     for (int i = 0; ok && sched.get(i, KB, w); ++i) {
       const Tile t = decode<TM>(bk, p, w.tile);
       const int steps = steps_of(t);
-      auto load_weights = [&](int kb) {
-        const int s = kb & (STAGES - 1);
+      auto load_weights = [&](int kb, int s) {
         uint8_t* to = smem + s * STAGE_BYTES;
         mbar_arrive_expect_tx(&full_bar[s], B_BYTES + steps * 16 * BK);
         if (GATED) {
@@ -224,17 +229,16 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_few_rows_kernel(
           tma_load_3d(to, &tm_b0, &full_bar[s], kb * BK, t.nb * BN, t.e);
         }
       };
-      if (!waited) {  // the weights of the first blocks do not depend on the launch before
+      if (!waited) {  // when it follows, the first blocks' weights do not depend on the other
         early = min(STAGES, w.kb1 - w.kb0);
         if (elect_one())
-          for (int kb = w.kb0; kb < w.kb0 + early; ++kb) load_weights(kb);
+          for (int j = 0; j < early; ++j) load_weights(w.kb0 + j, j);
         __syncwarp();
         wait_for_previous();
         waited = true;
       }
 #pragma unroll 1
-      for (int kb = w.kb0; kb < w.kb1; ++kb) {
-        const int s = kb & (STAGES - 1);
+      for (int kb = w.kb0; kb < w.kb1; ++kb, s = (s + 1) & (STAGES - 1)) {
         const uint32_t par = (fills >> s) & 1u;
         const bool ahead = early > 0;
         if (!ahead && !await(&done_bar[s], par ^ 1u, 51, w.tile)) {
@@ -243,7 +247,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_few_rows_kernel(
         }
         uint8_t* rows = smem + s * STAGE_BYTES + B_BYTES;
         if (elect_one()) {
-          if (!ahead) load_weights(kb);
+          if (!ahead) load_weights(kb, s);
           for (int g = 0; g < steps; ++g)
             tma_load_2d(rows + g * 16 * BK, &tm_a, &full_bar[s], kb * BK, t.row0 + g * 16);
         }
@@ -267,12 +271,12 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_few_rows_kernel(
     const uint64_t r_desc = sw128_kmajor_desc(smem_addr(smem) + B_BYTES);
     uint32_t fills = 0;  // stage s's next fill, and its accumulators' next use
     bool ok = true, issued = false;
+    int s = 0;  // the next block's stage
     Piece w;
     for (int i = 0; ok && sched.get(i, KB, w); ++i) {
       const uint32_t idesc = idesc_e4m3_f32(128, 16 * steps_of(decode<TM>(bk, p, w.tile)));
 #pragma unroll 1
-      for (int kb = w.kb0; kb < w.kb1; ++kb) {
-        const int s = kb & (STAGES - 1);
+      for (int kb = w.kb0; kb < w.kb1; ++kb, s = (s + 1) & (STAGES - 1)) {
         const uint32_t par = (fills >> s) & 1u;
         if (!await(&full_bar[s], par, 52, w.tile) || !await(&tempty_bar[s], par ^ 1u, 52, w.tile)) {
           ok = false;
@@ -313,7 +317,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_few_rows_kernel(
       const float* s0 = p.w_scale0 + (w_row + (GATED ? t.nb : 2 * t.nb)) * KB;
       const float* s1 = GATED ? p.w_scale1 + (w_row + t.nb) * KB
                               : p.w_scale0 + (w_row + min(2 * t.nb + 1, p.nsb - 1)) * KB;
-      for (int k0 = w.kb0; k0 < w.kb1; k0 += 4) {
+      for (int k0 = w.kb0 & ~3; k0 < w.kb1; k0 += 4) {
         float4 a[2];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -351,6 +355,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_few_rows_kernel(
     float* stage_out = reinterpret_cast<float*>(smem + STAGES * STAGE_BYTES);
     uint32_t fills = 0;  // bit s: parity of stage s's next fill
     uint32_t turns = 0, oph = 0, jph = 0;
+    int s = 0;  // the next block's stage
     bool ok = true;
     Piece w;
     for (int i = 0; ok && sched.get(i, KB, w); ++i) {
@@ -362,17 +367,17 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_few_rows_kernel(
 #pragma unroll
       for (int c = 0; c < TM; ++c) acc[c] = 0.f;
 #pragma unroll 1
-      for (int kb = w.kb0; kb < w.kb1; ++kb) {
-        const int s = kb & (STAGES - 1);
+      for (int kb = w.kb0; kb < w.kb1; ++kb, s = (s + 1) & (STAGES - 1)) {
         const uint32_t b = turns & 1u;
-        if ((s == 0 && !await(&sfull_bar[b], (turns >> 1) & 1u, 54, tile)) ||
+        const bool turn = (kb & 3) == 0 || kb == w.kb0;  // the first of the 4 blocks' scales
+        if ((turn && !await(&sfull_bar[b], (turns >> 1) & 1u, 54, tile)) ||
             !await(&done_bar[s], (fills >> s) & 1u, 55, tile)) {
           ok = false;
           break;
         }
         fills ^= 1u << s;
         tc_fence_after();
-        const float4* f = reinterpret_cast<const float4*>(scale_s[b][s][half]);
+        const float4* f = reinterpret_cast<const float4*>(scale_s[b][kb & 3][half]);
         const uint32_t from = ta + static_cast<uint32_t>(2 * s * TM);
 #pragma unroll
         for (int g = 0; g < TM / 16; ++g)
@@ -393,7 +398,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_few_rows_kernel(
           }
         tc_fence_before();
         arrive_if(&tempty_bar[s], first);
-        if (s == STAGES - 1 || kb == w.kb1 - 1) {  // every lane has read the 4 blocks' scales
+        if ((kb & 3) == 3 || kb == w.kb1 - 1) {  // every lane has read the 4 blocks' scales
           __syncwarp();
           arrive_if(&sfree_bar[b], first);
           ++turns;
@@ -407,22 +412,21 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_few_rows_kernel(
 #pragma unroll
         for (int c = 0; c < TM; ++c)
           if (c < valid) __stcg(to + c * BN, acc[c]);
-        const int64_t tile0 = static_cast<int64_t>(tile) * sched.groups;
+        const int64_t tile0 = static_cast<int64_t>(tile) * KB;
         // its pieces' CTAs; each has the tile as its run's first, but for the first of them when
         // that one's run starts in a tile before
-        const int c0 = sched.owner(tile0), c1 = sched.owner(tile0 + sched.groups - 1);
+        const int c0 = sched.owner(tile0), c1 = sched.owner(tile0 + KB - 1);
         const bool starts = sched.begin(c0) == tile0;
-        __threadfence();
         __syncwarp();
         arrive_if(&join_bar[0], first);
         if (warp == CTRL_WARPS) {
           if (!await(&join_bar[0], jph, 57, tile)) break;
           if (lane == 0) {
-            __threadfence();
-            const unsigned before = atomicAdd(p.arrivals + tile, 1u);
+            // release: the sums of all the block's warps, which the barrier has brought here;
+            // acquire: the other blocks' sums, for the warps that the next barrier lets go
+            const unsigned before = add_acq_rel(p.arrivals + tile, 1u);
             const int is_last = before == static_cast<unsigned>(c1 - c0);
             if (is_last) p.arrivals[tile] = 0u;  // as the next launch wants it
-            __threadfence();
             last_s = is_last;
           }
           __syncwarp();
@@ -431,7 +435,6 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_few_rows_kernel(
         if (!await(&join_bar[1], jph, 58, tile)) break;
         jph ^= 1u;
         if (last_s != 0) {
-          __threadfence();
 #pragma unroll 1
           for (int m = ew; m < valid; m += EPI_WARPS) {
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
@@ -492,11 +495,11 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_few_rows_kernel(
 
 template <int MODE>
 cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b0, const CUtensorMap& b1,
-                   const Fp8Params& p, bool follows, cudaStream_t st) {
+                   const Fp8Params& p, cudaStream_t st) {
   // at most one ragged row block per bucket, the rest full; each can be cut into pieces
   const int64_t tiles = (p.rows / TM + (p.rows < p.E ? p.rows : p.E)) * p.n_blocks;
   return launch_product(fp8_few_rows_kernel<MODE>, tiles * ((p.kb + 3) / 4), THREADS, DYN_SMEM,
-                        follows, st, a, b0, b1, p);
+                        st, a, b0, b1, p);
 }
 
 }  // namespace
@@ -512,8 +515,7 @@ cudaError_t launch_fp8_few_rows(const Fp8Gemm& g, const Fp8Params& p, cudaStream
     return cudaErrorInvalidValue;
   }
   if (!gated) b1 = b0;
-  return gated ? launch<FP8_GATED>(a, b0, b1, p, g.follows, st)
-               : launch<FP8_LINEAR>(a, b0, b1, p, g.follows, st);
+  return gated ? launch<FP8_GATED>(a, b0, b1, p, st) : launch<FP8_LINEAR>(a, b0, b1, p, st);
 }
 
 }  // namespace moe

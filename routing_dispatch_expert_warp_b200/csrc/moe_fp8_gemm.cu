@@ -141,13 +141,14 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
   const int lane = threadIdx.x & 31;
 
   if (warp == 0) {
-    build_buckets<BM>(bk, p, lane);
     if (lane == 0) {
       prefetch_tensormap(&tm_a);
       prefetch_tensormap(&tm_a32);
       prefetch_tensormap(&tm_b0);
       if (GATED) prefetch_tensormap(&tm_b1);
     }
+    if (!p.follows) wait_for_previous();
+    build_buckets<BM>(bk, p, lane);
   } else if (warp == 1) {
     tmem_alloc(&tmem_base_s, TMEM_COLS);
     tmem_relinquish();
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
           tma_load_3d(sb, &tm_b0, &full_bar[s], kb * BK, t.nb * BN, t.e);
         }
       };
-      if (!waited) {  // the weights of the first blocks do not depend on the launch before
+      if (!waited) {  // when it follows, the first blocks' weights do not depend on the other
         early = min(STAGES, KB);
         if (elect_one())
           for (int kb = 0; kb < early; ++kb) load_weights(kb);
@@ -462,11 +463,11 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
 
 template <int MODE>
 cudaError_t launch(const CUtensorMap& a, const CUtensorMap& a32, const CUtensorMap& b0,
-                   const CUtensorMap& b1, const Fp8Params& p, bool follows, cudaStream_t st) {
+                   const CUtensorMap& b1, const Fp8Params& p, cudaStream_t st) {
   // at most one ragged row block per bucket, the rest full
   const int64_t tiles = (p.rows / BM + (p.rows < p.E ? p.rows : p.E)) * p.n_blocks;
-  return launch_product(fp8_grouped_gemm_kernel<MODE>, tiles, THREADS, DYN_SMEM, follows, st, a,
-                        a32, b0, b1, p);
+  return launch_product(fp8_grouped_gemm_kernel<MODE>, tiles, THREADS, DYN_SMEM, st, a, a32, b0,
+                        b1, p);
 }
 
 }  // namespace
@@ -503,6 +504,7 @@ cudaError_t launch_fp8_gemm(const Fp8Gemm& g, void* ws, uint64_t wait_ns, cudaSt
   p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kFp8PartialsOffset);
   p.status = static_cast<DevStatus*>(ws);
   p.wait_ns = wait_ns;
+  p.follows = g.follows;
   if (g.rows <= kFewRows * static_cast<int64_t>(g.E)) return launch_fp8_few_rows(g, p, st, why);
   CUtensorMap a, a32, b0, b1;
   if (!map_rows(&a, g.a, g.rows, g.K, BM) || !map_rows(&a32, g.a, g.rows, g.K, 32) ||
@@ -512,8 +514,8 @@ cudaError_t launch_fp8_gemm(const Fp8Gemm& g, void* ws, uint64_t wait_ns, cudaSt
     return cudaErrorInvalidValue;
   }
   if (!gated) b1 = b0;
-  return gated ? launch<FP8_GATED>(a, a32, b0, b1, p, g.follows, st)
-               : launch<FP8_LINEAR>(a, a32, b0, b1, p, g.follows, st);
+  return gated ? launch<FP8_GATED>(a, a32, b0, b1, p, st)
+               : launch<FP8_LINEAR>(a, a32, b0, b1, p, st);
 }
 
 }  // namespace moe

@@ -29,6 +29,7 @@ struct Fp8Params {
   float* partials;        // 2 slots a CTA, see the kernels
   DevStatus* status;
   uint64_t wait_ns;
+  bool follows;  // see Fp8Gemm
 };
 
 // The kernel for buckets of few rows (moe_fp8_few.cu).
@@ -51,12 +52,9 @@ enum Mode { FP8_LINEAR = 0, FP8_GATED = 1 };
 constexpr int SLOT_FLOATS = 64 * BN;  // partial sums of a piece
 
 // Programmatic dependent launch: let the next launch's blocks start as this one's leave their
-// SMs; wait until the launch before has completed (at once when there is none to wait for).
+// SMs.
 __device__ __forceinline__ void let_next_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void wait_for_previous() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // 32 lanes x 16 columns of tensor memory, on their way until tmem_ld_wait().
@@ -92,10 +90,9 @@ __device__ __forceinline__ void arrive_if(uint64_t* bar, uint32_t who) {
 // 4 scales from block kb on (0 past the last of n).
 __device__ __forceinline__ float4 scales4(const float* s, int kb, int n) {
   if ((n & 3) == 0)
-    return kb < n ? __ldg(reinterpret_cast<const float4*>(s + kb))
-                  : make_float4(0.f, 0.f, 0.f, 0.f);
-  return make_float4(kb < n ? __ldg(s + kb) : 0.f, kb + 1 < n ? __ldg(s + kb + 1) : 0.f,
-                     kb + 2 < n ? __ldg(s + kb + 2) : 0.f, kb + 3 < n ? __ldg(s + kb + 3) : 0.f);
+    return kb < n ? *reinterpret_cast<const float4*>(s + kb) : make_float4(0.f, 0.f, 0.f, 0.f);
+  return make_float4(kb < n ? s[kb] : 0.f, kb + 1 < n ? s[kb + 1] : 0.f,
+                     kb + 2 < n ? s[kb + 2] : 0.f, kb + 3 < n ? s[kb + 3] : 0.f);
 }
 __device__ __forceinline__ float pick(const float4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
@@ -249,26 +246,15 @@ inline bool map_weights(CUtensorMap* m, const void* base, int64_t E, int64_t N, 
   return encode(m, 3, base, dims, strides, box);
 }
 
-// One launch of at most one block per SM and `most` blocks; `follows`: see Fp8Gemm.
+// One launch of at most one block per SM and `most` blocks.
 template <typename... Params, typename... Args>
 cudaError_t launch_product(void (*kernel)(Params...), int64_t most, int threads, int smem,
-                           bool follows, cudaStream_t st, const Args&... args) {
+                           cudaStream_t st, const Args&... args) {
   cudaError_t err = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (err != cudaSuccess) return err;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(most < sm_count() ? most : sm_count()));
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = follows ? 1 : 0;
-  err = cudaLaunchKernelEx(&cfg, kernel, args...);
-  if (err == cudaSuccess) note_launch();
-  return err;
+  return launch_overlapping(kernel, most < sm_count() ? most : sm_count(), threads, smem, st,
+                            args...);
 }
 
 }  // namespace

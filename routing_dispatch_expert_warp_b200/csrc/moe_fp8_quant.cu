@@ -43,7 +43,7 @@ struct Piece {
     const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) +
                                                     elem * (BF16 ? 2 : 4));
 #pragma unroll
-    for (int i = 0; i < (BF16 ? 2 : 4); ++i) v[i] = __ldg(p + i);
+    for (int i = 0; i < (BF16 ? 2 : 4); ++i) v[i] = p[i];
   }
   __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -129,9 +129,9 @@ struct Quant {
 // inside [0, rows_out); without one to the row of its own index.
 template <bool BF16>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(
-    const void* __restrict__ x, int64_t rows_in, int cols, int chunks,
-    const int32_t* __restrict__ assign_row, int k, int64_t rows_out, uint8_t* __restrict__ q,
-    float* __restrict__ scale) {
+    const void* x, int64_t rows_in, int cols, int chunks, const int32_t* assign_row, int k,
+    int64_t rows_out, uint8_t* q, float* scale) {
+  wait_for_previous();
   const int lane = threadIdx.x & 31;
   const int64_t items = rows_in * chunks;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(
     const int64_t row = item / chunks;
     const int col = static_cast<int>(item - row * chunks) * 512 + lane * 16;
     int32_t mine = -1;
-    if (assign_row != nullptr && lane < k) mine = __ldg(assign_row + row * k + lane);
+    if (assign_row != nullptr && lane < k) mine = assign_row[row * k + lane];
     Piece<BF16> p;
     if (col < cols) p.load(x, row * cols + col);
     else p.zero();
@@ -165,8 +165,9 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(
 // registers between the two passes over it.
 template <bool BF16>
 __global__ void __launch_bounds__(256) quantize_weights_kernel(
-    const void* __restrict__ w, int64_t n, int64_t cols, int nb, int kb, int64_t blocks,
-    uint8_t* __restrict__ q, float* __restrict__ scale) {
+    const void* w, int64_t n, int64_t cols, int nb, int kb, int64_t blocks, uint8_t* q,
+    float* scale) {
+  wait_for_previous();
   __shared__ uint32_t part[2][8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int parity = 0;
@@ -208,16 +209,11 @@ cudaError_t launch_fp8_quantize_rows(int dtype, const void* x, int64_t rows_in, 
   const int chunks = static_cast<int>((cols + 511) / 512);
   const int64_t blocks = (rows_in * chunks + 7) / 8;
   const int64_t most = static_cast<int64_t>(sm_count()) * 64;
-  const unsigned grid = static_cast<unsigned>(blocks < most ? blocks : most);
+  const int64_t grid = blocks < most ? blocks : most;
   uint8_t* out = static_cast<uint8_t*>(q);
-  if (dtype == MOE_BF16)
-    quantize_rows_kernel<true><<<grid, 256, 0, st>>>(x, rows_in, static_cast<int>(cols), chunks,
-                                                     assign_row, k, rows_out, out, scale);
-  else
-    quantize_rows_kernel<false><<<grid, 256, 0, st>>>(x, rows_in, static_cast<int>(cols), chunks,
-                                                      assign_row, k, rows_out, out, scale);
-  note_launch();
-  return cudaGetLastError();
+  return launch_overlapping(
+      dtype == MOE_BF16 ? quantize_rows_kernel<true> : quantize_rows_kernel<false>, grid, 256, 0,
+      st, x, rows_in, static_cast<int>(cols), chunks, assign_row, k, rows_out, out, scale);
 }
 
 cudaError_t launch_fp8_quantize_weights(int dtype, const void* w, int64_t E, int64_t n,
@@ -225,14 +221,11 @@ cudaError_t launch_fp8_quantize_weights(int dtype, const void* w, int64_t E, int
   const int nb = static_cast<int>((n + 127) / 128), kb = static_cast<int>((cols + 127) / 128);
   const int64_t blocks = E * nb * kb;
   const int64_t most = static_cast<int64_t>(sm_count()) * 64;
-  const unsigned grid = static_cast<unsigned>(blocks < most ? blocks : most);
+  const int64_t grid = blocks < most ? blocks : most;
   uint8_t* out = static_cast<uint8_t*>(q);
-  if (dtype == MOE_BF16)
-    quantize_weights_kernel<true><<<grid, 256, 0, st>>>(w, n, cols, nb, kb, blocks, out, scale);
-  else
-    quantize_weights_kernel<false><<<grid, 256, 0, st>>>(w, n, cols, nb, kb, blocks, out, scale);
-  note_launch();
-  return cudaGetLastError();
+  return launch_overlapping(
+      dtype == MOE_BF16 ? quantize_weights_kernel<true> : quantize_weights_kernel<false>, grid,
+      256, 0, st, w, n, cols, nb, kb, blocks, out, scale);
 }
 
 }  // namespace moe

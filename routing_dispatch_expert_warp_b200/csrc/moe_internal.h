@@ -186,8 +186,8 @@ struct Fp8Gemm {
   void* out;                // [rows, N] bf16
   void* h;                  // [rows, N] e4m3
   float* h_scale;           // [rows, ceil(N / 128)]
-  bool follows;             // the launch before in the stream is the product that made a: this
-                            // one's blocks may start as that one's end
+  bool follows;             // the launch before in the stream is the product that made a: only
+                            // a and a_scale depend on it
 };
 // Workspace of the fp8 products: the status record, then arrival counters (zero between
 // calls), then partial sums.
@@ -211,6 +211,26 @@ int ffn_kernel();
 
 // Process-wide count of this library's kernel launches (every launch site calls it once).
 void note_launch();
+
+// A launch whose blocks may start while the launch before in the stream is ending: each begins
+// with wait_for_previous() (moe_device.cuh).
+template <typename... Params, typename... Args>
+cudaError_t launch_overlapping(void (*kernel)(Params...), int64_t blocks, int threads, int smem,
+                               cudaStream_t st, const Args&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (err == cudaSuccess) note_launch();
+  return err;
+}
 
 // Allocation-free dispatch: scratch lives in a fixed device array (moe_dispatch.cu).
 constexpr size_t kStaticDispatchHistBytes = size_t(1) << 20;  // 1 MiB of block histograms

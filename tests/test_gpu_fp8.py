@@ -633,6 +633,69 @@ def test_layer_captured_into_a_graph():
     layer.check_device_error()
 
 
+@pytest.mark.parametrize("rows", [3, 300], ids=["few", "many"])
+def test_calls_wait_for_whatever_came_before(rows):
+    """Launches may start while the one before is ending.  Their inputs come late here from a
+    kernel, a copy from the host and a memset, eagerly and captured, on their stream and from
+    another one that it waits for."""
+    E, N, K = 2, 520, 1040
+    x = torch.randn((rows, K), generator=gen(7)).bfloat16()
+    w = torch.randn((E, N, K), generator=gen(8)) / K ** 0.5
+    counts = [rows - 1, 1]
+    ref_q, ref_s = quantized_rows(x)
+    w_q, w_s = quantized_weights(w)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    first, count = torch.tensor([0, rows - 1], **i32), torch.tensor(counts, **i32)
+    ws = M.alloc_fp8_workspace()
+    want = torch.empty((rows, N), dtype=torch.bfloat16, device="cuda")
+    M.moe_fp8_grouped_gemm(ref_q, ref_s, first, count, w_q, w_s, want, ws)
+    check_product(want, ref_q, ref_s, w_q, w_s, [0, rows - 1], counts)
+    host, host_count = x.pin_memory(), torch.tensor(counts, dtype=torch.int32).pin_memory()
+    dx, dw = torch.empty_like(x, device="cuda"), w.cuda()
+    q, s = torch.empty_like(ref_q), torch.empty_like(ref_s)
+    wq, wsc = torch.empty_like(w_q), torch.empty_like(w_s)
+    out, dcount = torch.empty_like(want), torch.empty_like(count)
+    other = torch.cuda.Stream()
+
+    def step():
+        for t in (dx, s, wsc):
+            t.fill_(float("nan"))
+        torch.cuda._sleep(200_000)
+        dx.copy_(host, non_blocking=True)
+        M.moe_fp8_quantize_rows(dx, q, s)
+        torch.cuda._sleep(200_000)
+        here = torch.cuda.current_stream()
+        other.wait_stream(here)
+        with torch.cuda.stream(other):
+            torch.cuda._sleep(200_000)
+            M.moe_fp8_quantize_weights(dw, wq, wsc)
+        here.wait_stream(other)
+        dcount.zero_()
+        dcount.copy_(host_count, non_blocking=True)
+        M.moe_fp8_grouped_gemm(q, s, first, dcount, wq, wsc, out, ws)
+
+    def check():
+        torch.cuda.synchronize()
+        M.moe_check_device_error(ws)
+        assert torch.equal(out, want)
+        out.fill_(0)
+        for t in (q, wq):
+            t.view(torch.uint8).fill_(0x7F)
+        dcount.fill_(0)
+
+    side = torch.cuda.Stream()
+    for stream in (torch.cuda.current_stream(), side):
+        with torch.cuda.stream(stream):
+            step()
+        check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    for _ in range(3):
+        graph.replay()
+        check()
+
+
 def test_layer_is_a_layer():
     """What MoELayer offers beside forward: a router weight changed in place, the counters of
     second choices, a captured forward."""

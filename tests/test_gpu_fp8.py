@@ -61,7 +61,8 @@ def values(shape, dtype, seed, kind="normal"):
 # ------------------------------------------------------------------ rows
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("rows,cols", [(1, 16), (1, 128), (3, 144), (7, 1520), (129, 528),
-                                       (1000, 4096), (2, 16384)])
+                                       (1000, 4096), (2, 16384), (1003, 16), (77, 128),
+                                       (301, 176), (6, 256), (5, 272)])
 @pytest.mark.parametrize("kind", ["normal", "outliers", "spread", "tiny", "borders", "zero"])
 def test_rows(rows, cols, dtype, kind):
     x = values((rows, cols), dtype, rows + cols, kind)
@@ -132,7 +133,8 @@ def test_no_rows():
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("T,d,E,k,cf", [(1, 16, 1, 1, 0.0), (1, 4096, 8, 2, 0.0),
                                         (37, 1520, 13, 8, 0.5), (600, 656, 256, 8, 1.0),
-                                        (64, 7168, 4, 3, 0.0)])
+                                        (64, 7168, 4, 3, 0.0), (203, 32, 16, 8, 0.7),
+                                (50, 128, 8, 5, 0.0), (77, 240, 8, 2, 0.6)])
 def test_permute_writes_the_kept_picks_rows(T, d, E, k, cf, dtype):
     g = gen(T + d)
     cfg = M.make_config(T, d, 128, E, k, capacity_factor=cf,

@@ -5,7 +5,7 @@
 // 128 places, 4 rows cost the tensor cores and the epilogue as much as 128 (and power, which
 // the clocks pay for): a DeepSeek-shaped decode step of 4 rows an expert takes 2.08 ms there and
 // 1.60 to 1.66 here, where a block of 128 costs the epilogue 16 sums a thread; that is 6.6 to 6.9
-// TB/s.  32 experts of 7168 x 2048 with 128 rows take 79 us, 5.9 TB/s; one token through the
+// TB/s.  32 experts of 7168 x 2048 with 128 rows take 78 us, 6.0 TB/s; one token through the
 // Mixtral-8x7B shaped experts 67, of which reading the weights is 54.
 //
 // FP8_LINEAR: the halves are 128 output columns each.  FP8_GATED: 128 rows of W_gate and the
@@ -54,15 +54,16 @@ struct Schedule {
   __device__ Schedule(int total, int KB) {
     const int G = static_cast<int>(gridDim.x);
     const int full = total / G, rest = total - full * G;
-    // Cutting saves the blocks of the reduction that the last round leaves unused and costs a
-    // join; and the tiles of a last round that is half full share the memory's whole rate
-    // anyway.  (Two experts' rows, K = 4096, N = 28672, 16 blocks saved: 44.1 us whole, 45.1 cut;
-    // N = 8192, 18 saved: 20.9 and 21.5; N = 4096, 25 saved: 18.8 and 16.6; N = 20480, 29 saved:
-    // 42.0 and 35.6.)
-    constexpr int join_blocks = 20;
-    const bool cut = full < 2 && rest != 0 &&
-                     static_cast<int64_t>((full + 1) * G - total) * KB >
-                         static_cast<int64_t>(join_blocks) * G;
+    // Whole tiles: the last round's `rest` tiles share the memory's rate, but an SM alone still
+    // needs 2/5 of the time for a block that it needs when all SMs load.  Cut tiles keep all SMs
+    // loading to the end and cost a join, as long as 4 blocks.  (Two experts' rows, K
+    // = 4096, 148 SMs: N = 20480, 12 left over, 42.0 us whole, 35.6 cut; N = 4096, 32 left over,
+    // 18.8 and 16.6; N = 8192, 64 left over, 20.9 and 21.5; N = 28672, 76 left over, 44.1 and
+    // 45.1.  Seven rounds of 16 experts, 14336 x 4096, 8 left over: 146.9 and 143.2.)  Over many
+    // rounds it gains little, and runs of neighbouring tiles lose that again (27 rounds of the
+    // DeepSeek-shaped decode step: 1588 us and 1603).
+    const bool cut = full < 10 && rest != 0 &&
+                     static_cast<int64_t>(2 * G - 5 * rest) * KB > 20 * G;
     rounds = cut ? 0 : full + (static_cast<int>(blockIdx.x) < rest ? 1 : 0);
     units = cut ? static_cast<int64_t>(total) * KB : 0;
     ctas = units < 4 * G ? static_cast<int>((units + 3) >> 2) : G;
@@ -425,9 +426,10 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_few_rows_kernel(
           if (lane == 0) {
             // release: the sums of all the block's warps, which the barrier has brought here;
             // acquire: the other blocks' sums, for the warps that the next barrier lets go
-            const unsigned before = add_acq_rel(p.arrivals + tile, 1u);
+            // (c0 tells cut tiles apart: only the last tile of a run goes on in the next one)
+            const unsigned before = add_acq_rel(p.arrivals + c0, 1u);
             const int is_last = before == static_cast<unsigned>(c1 - c0);
-            if (is_last) p.arrivals[tile] = 0u;  // as the next launch wants it
+            if (is_last) p.arrivals[c0] = 0u;  // as the next launch wants it
             last_s = is_last;
           }
           __syncwarp();

@@ -240,6 +240,8 @@ GEMM = [  # counts, N, K
     ([200, 0, 0, 1, 0, 0, 17, 0], 1000, 1520),   # one long bucket among few rows
     ([64, 16, 15, 17, 48, 49, 63, 65, 0, 1, 0, 2], 520, 272),
     ([5], 14336, 4096),
+    ([4] * 32, 7168, 2048),    # seven rounds of tiles on 148 SMs, the last one nearly empty
+    ([1, 30, 2, 0, 9], 30000, 1040),
 ]
 
 

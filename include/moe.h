@@ -587,9 +587,11 @@ moe_status_t moe_fp8_quantize_weights(int32_t dtype, int64_t E, int64_t N, int64
                                       const void* w, void* q, float* scale, void* stream);
 
 /* Workspace of the two calls below: one size whatever the problem, for the current device.
- * Initialise it once after allocating (and again after MOE_ERR_TIMEOUT).  Its status word is
- * read by moe_check_device_error.  Calls on one workspace must not overlap: give each stream
- * and each captured graph that may run beside another its own. */
+ * Initialise it once after allocating, and again after any error that moe_check_device_error
+ * reports of it: a wait that ran out leaves counters behind that the next call would go by, and
+ * the status word keeps the first error alone, so another error may hide that one.  Calls on one
+ * workspace must not overlap: give each stream and each captured graph that may run beside
+ * another its own. */
 moe_status_t moe_fp8_workspace_size(size_t* bytes);
 moe_status_t moe_fp8_workspace_init(void* ws, size_t ws_bytes, void* stream);
 

@@ -337,12 +337,21 @@ class MoELayerFp8(MoELayer):
     __call__ = forward
 
     def check_device_error(self, stream: Optional[torch.cuda.Stream] = None) -> None:
-        """Report (MoEError) and clear the kernel-side errors of the forwards so far."""
+        """Report (MoEError) and clear the kernel-side errors of the forwards so far: of both
+        workspaces, the first one's error first.  Any error of the products' workspace has it
+        initialised again: a wait that ran out leaves counters behind, and the status, which
+        keeps the first error alone, may show another."""
         check_error = _abi.lib().moe_check_device_error
-        _call(check_error, self.ws.device, stream, self.ws.data_ptr(), self.ws.numel())
-        try:
-            _call(check_error, self.ws.device, stream, self.fp8_ws.data_ptr(),
-                  self.fp8_ws.numel())
-        except _abi.MoEError:
-            moe_fp8_workspace_init(self.fp8_ws, stream)  # (a run-out wait leaves counters behind)
-            raise
+        found = []
+        for ws in (self.ws, self.fp8_ws):
+            try:
+                _call(check_error, ws.device, stream, ws.data_ptr(), ws.numel())
+            except _abi.MoEError as e:
+                found.append(e)
+                if ws is self.fp8_ws:
+                    try:
+                        moe_fp8_workspace_init(ws, stream)
+                    except _abi.MoEError as failed:
+                        found.append(failed)
+        if found:
+            raise found[0]

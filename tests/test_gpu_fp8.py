@@ -795,3 +795,27 @@ def test_two_ffn_graphs_beside_each_other(counts):
     for graph, stream, args, ws, want in runs:
         M.moe_check_device_error(ws)
         assert torch.equal(args[8], want)
+
+
+@pytest.mark.parametrize("layer_code,code", [(1, 1), (1, 4), (0, 4)],
+                         ids=["both ran out", "bad bucket in both", "bad bucket alone"])
+def test_check_restores_the_workspace_whatever_the_errors(layer_code, code):
+    """Counters of cut tiles left behind, with an error of the layer's own workspace beside the
+    products', or with a bad bucket recorded before the wait that ran out."""
+    shape = W.reduced(W.MIXTRAL_8X7B, 1, 1024, 512)
+    inp = W.make_inputs(shape, device="cuda")
+    cfg = M.config_from_shape(shape)
+    experts = M.Fp8Experts.quantize(inp.w_gate, inp.w_up, inp.w_down)
+    layer = M.MoELayerFp8(cfg, inp.w_router, experts, inp.logit_bias)
+    want = layer(inp.x).clone()
+    layer.check_device_error()
+    words = layer.fp8_ws[:4096].view(torch.int32)
+    words[64:128] = 1  # counters of cut tiles
+    words[0] = code
+    layer.ws[:4].view(torch.int32)[0] = layer_code
+    with pytest.raises(M.MoEError) as e:
+        layer.check_device_error()
+    assert e.value.status == (5 if layer_code else 6)
+    assert not words.any()
+    assert torch.equal(layer(inp.x), want)
+    layer.check_device_error()

@@ -65,34 +65,39 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _call(fn, device: torch.device, stream, *args) -> None:
-    """fn(*args, stream) with the tensors' device current."""
-    index = device.index
+def _handle(device: torch.device, stream) -> int:
+    """The handle of `stream` (None: the device's current stream)."""
     if device.type != "cuda":
         raise ValueError(f"the tensors must be on a CUDA device, got {device}")
     if stream is None:
-        raw = _raw_stream(index)
-    elif isinstance(stream, torch.cuda.Stream):
+        return _raw_stream(device.index)
+    if isinstance(stream, torch.cuda.Stream):
         if stream.device != device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        raw = stream.cuda_stream
-    else:
-        raw = int(stream)
-    if index == _current_device():
+        return stream.cuda_stream
+    return int(stream)
+
+
+def _call(fn, device: torch.device, stream, *args) -> None:
+    """fn(*args, stream) with the tensors' device current."""
+    raw = _handle(device, stream)
+    if device.index == _current_device():
         status = fn(*args, raw)
     else:
-        with torch.cuda.device(index):
+        with torch.cuda.device(device.index):
             status = fn(*args, raw)
     if status:
         check(status)
 
 
-def _allocating_on(stream):
-    """New tensors' memory comes from work that `stream` has already been given (another
-    stream's may still be in use there when `stream` writes to it)."""
-    if stream is None or isinstance(stream, torch.cuda.Stream):
+def _allocating_on(stream, device):
+    """New tensors' memory comes from work that `stream`, one of `device`, has already been given
+    (another stream's may still be in use there when `stream` writes to it)."""
+    if stream is None:
+        return torch.cuda.device(device)
+    if isinstance(stream, torch.cuda.Stream):
         return torch.cuda.stream(stream)
-    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream)))
+    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=device))
 
 
 def _max_rows(cfg: MoeConfig) -> int:
@@ -152,7 +157,7 @@ def alloc_fp8_workspace(device="cuda", stream=None) -> torch.Tensor:
     """A workspace, initialised.  Calls on one workspace must not overlap: one for each stream,
     and for each captured graph that may run beside another."""
     n = fp8_workspace_size(device)
-    with _allocating_on(stream):
+    with _allocating_on(stream, device):
         ws = torch.empty(n, dtype=torch.uint8, device=device)
     moe_fp8_workspace_init(ws, stream)
     return ws
@@ -225,7 +230,7 @@ class Fp8Experts:
         """Quantise a layer's fp32 or bf16 weights."""
         parts = []
         for w in (w_gate, w_up, w_down):
-            with _allocating_on(stream):
+            with _allocating_on(stream, w.device):
                 q = torch.empty(w.shape, dtype=E4M3, device=w.device)
                 s = torch.empty(fp8_scale_shape(w.shape), dtype=torch.float32, device=w.device)
             moe_fp8_quantize_weights(w, q, s, stream)
@@ -318,6 +323,18 @@ class MoELayerFp8(MoELayer):
             self.bufs = self.fp8_bufs.layer
             self._structs = self.bufs.as_struct(True), self.fp8_bufs.as_struct()
             self.resplit_router()
+
+    def resplit_router(self, stream=None) -> None:
+        dev = self.experts.w_gate.device
+        raw = _handle(dev, stream)
+        with _allocating_on(stream, dev):
+            super().resplit_router(raw)
+
+    def pick_rank_counts(self, group_of_expert=None, stream=None):
+        dev = self.experts.w_gate.device
+        raw = _handle(dev, stream)
+        with _allocating_on(stream, dev):
+            return super().pick_rank_counts(group_of_expert, raw)
 
     def inputs(self, x) -> MoeLayerInputs:
         b, split = self.logit_bias, self.w_router_split

@@ -22,6 +22,7 @@ class FakeLibrary:
     def __init__(self):
         self.status, self.calls, self.last = {}, [], b""
         self.device = 0  # the current device, as torch.cuda.device sets it
+        self.streams = [1000, 1001]  # each device's current stream
 
     def moe_check_device_error(self, ws, n, stream):
         self.calls.append(("check", ws, self.device, stream))
@@ -37,13 +38,85 @@ class FakeLibrary:
     def moe_last_error(self):
         return self.last
 
+    def moe_router_split_size(self, cfg, n):
+        ctypes.cast(n, ctypes.POINTER(ctypes.c_size_t))[0] = 4096
+        return 0
+
+    def moe_router_split(self, cfg, w, out, n, stream):
+        self.calls.append(("split", out, self.device, stream))
+        return 0
+
+    def moe_pick_rank_counts(self, cfg, idx, row, group, routed, kept, differs, ws, n, stream):
+        self.calls.append(("counts", ws, self.device, stream))
+        return 0
+
+    def moe_fp8_quantize_weights(self, dtype, E, N, K, w, q, scale, stream):
+        self.calls.append(("quantize", w, self.device, stream))
+        return 0
+
+    def moe_fp8_workspace_size(self, n):
+        ctypes.cast(n, ctypes.POINTER(ctypes.c_size_t))[0] = 4096
+        return 0
+
+
+class FakeStream:
+    def __init__(self, handle, device=None):
+        self.cuda_stream, self.device = handle, device
+
+
+class FakeTensor:
+    """A tensor of the fake library's devices: what the Python layer asks of one."""
+
+    def __init__(self, shape, dtype, device, at):
+        self.shape, self.dtype, self.device = torch.Size(shape), dtype, torch.device(device)
+        self.at = at  # (device, stream) whose memory it was given
+        self.address = id(self)
+
+    def data_ptr(self):
+        return self.address
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def is_contiguous(self):
+        return True
+
 
 @pytest.fixture
 def lib(monkeypatch):
     fake = FakeLibrary()
     monkeypatch.setattr(_abi, "lib", lambda: fake)
     monkeypatch.setattr(fp8, "_current_device", lambda: fake.device)
-    monkeypatch.setattr(fp8, "_raw_stream", lambda index: 1000 + index)
+    monkeypatch.setattr(fp8, "_raw_stream", lambda index: fake.streams[index])
+    monkeypatch.setattr(torch.cuda, "Stream", FakeStream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: FakeStream(
+        handle, torch.device("cuda", fake.device) if device is None else torch.device(device)))
+    monkeypatch.setattr(torch.cuda, "current_stream",
+                        lambda d=None: FakeStream(fake.streams[fake.device]))
+
+    def empty(*shape, dtype=None, device=None):
+        shape = shape[0] if len(shape) == 1 and not isinstance(shape[0], int) else shape
+        at = torch.device(device).index
+        return FakeTensor(shape, dtype, device, (at, fake.streams[at]))
+
+    monkeypatch.setattr(torch, "empty", empty)
+
+    @contextlib.contextmanager
+    def stream(s):
+        if s is None:
+            yield
+            return
+        device, fake.device = fake.device, s.device.index
+        before, fake.streams[s.device.index] = fake.streams[s.device.index], s.cuda_stream
+        try:
+            yield
+        finally:
+            fake.streams[s.device.index], fake.device = before, device
+
+    monkeypatch.setattr(torch.cuda, "stream", stream)
 
     @contextlib.contextmanager
     def device(d):
@@ -66,6 +139,16 @@ def bare_layer(index=0):
     """A layer without its constructor: what the methods under test read of it."""
     layer = object.__new__(M.MoELayerFp8)
     layer.ws, layer.fp8_ws = workspace(0x100, index), workspace(0x200, index)
+    layer.ws.is_contiguous = lambda: True
+    layer.cfg = M.make_config(64, 256, 128, 8, 2)
+
+    def on_device(dtype, *shape):
+        return FakeTensor(shape, dtype, f"cuda:{index}", None)
+
+    layer.w_router = on_device(torch.float32, 256, 8)
+    layer.experts = types.SimpleNamespace(w_gate=on_device(fp8.E4M3, 8, 128, 256))
+    layer.bufs = types.SimpleNamespace(topk_idx=on_device(torch.int32, 64, 2),
+                                       assign_row=on_device(torch.int32, 64, 2))
     return layer
 
 
@@ -126,3 +209,47 @@ def test_check_on_the_layers_device_and_stream(lib):
     checked(layer, lib, stream=77)
     assert [c[2:] for c in lib.calls] == [(1, 77)] * 3
     assert lib.device == 0
+
+
+# ------------------------------------------------------------------ devices and streams
+@pytest.mark.parametrize("stream,runs_on", [(None, 1001), (77, 77),
+                                            (FakeStream(88, torch.device("cuda", 1)), 88)],
+                         ids=["current", "handle", "stream"])
+def test_a_layers_calls_run_on_its_device(lib, stream, runs_on):
+    """The layer's device is not the current one; what a call allocates belongs to its stream."""
+    layer = bare_layer(1)
+    layer.resplit_router(stream)
+    counts = layer.pick_rank_counts(stream=stream)
+    assert [(c[0], *c[2:]) for c in lib.calls] == [("split", 1, runs_on), ("counts", 1, runs_on)]
+    for t in (layer.w_router_split, *counts):
+        assert t.at == (1, runs_on)
+    assert lib.device == 0 and lib.streams == [1000, 1001]
+
+
+def test_a_layer_refuses_a_stream_of_another_device(lib):
+    layer = bare_layer(1)
+    for call in (layer.resplit_router, layer.check_device_error,
+                 lambda s: layer.pick_rank_counts(stream=s)):
+        with pytest.raises(ValueError, match="stream"):
+            call(FakeStream(88, torch.device("cuda", 0)))
+    assert lib.calls == []
+
+
+@pytest.mark.parametrize("stream,runs_on", [(None, 1001), (77, 77)], ids=["current", "handle"])
+def test_new_tensors_belong_to_the_stream_on_their_own_device(lib, stream, runs_on):
+    """A stream's handle does not say its device: it is the tensors' one."""
+    w = [FakeTensor(s, torch.bfloat16, "cuda:1", None)
+         for s in ((2, 128, 256), (2, 128, 256), (2, 256, 128))]
+    ex = M.Fp8Experts.quantize(*w, stream)
+    ws = M.alloc_fp8_workspace("cuda:1", stream)
+    for t in (ex.w_gate, ex.gate_scale, ex.w_up, ex.up_scale, ex.w_down, ex.down_scale, ws):
+        assert t.at == (1, runs_on)
+    assert [(c[0], *c[2:]) for c in lib.calls] == [("quantize", 1, runs_on)] * 3 + [
+        ("init", 1, runs_on)]
+    assert lib.device == 0
+
+
+def test_weights_on_the_host_are_refused():
+    w = torch.zeros(1, 16, 16)
+    with pytest.raises(ValueError):
+        M.Fp8Experts.quantize(w, w, w)

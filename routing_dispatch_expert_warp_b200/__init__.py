@@ -131,14 +131,16 @@ def router_split_size(cfg) -> int:
     return n.value
 
 
-def router_split(cfg, w_router, stream=None) -> Optional[torch.Tensor]:
+def router_split(cfg, w_router, stream=None, out=None) -> Optional[torch.Tensor]:
     """The split router weight of w_router (a uint8 device tensor), or None when the layer
-    never uses the tensor-core router.  It stays valid while w_router is unchanged."""
+    never uses the tensor-core router.  It stays valid while w_router is unchanged.  out: the
+    tensor of an earlier call with this cfg, written again."""
     n = router_split_size(cfg)
     if n == 0:
         return None
-    out = torch.empty(n, dtype=torch.uint8, device=w_router.device)
-    check(_lib().moe_router_split(ctypes.byref(cfg), _ptr(w_router), _ptr(out), n,
+    if out is None:
+        out = torch.empty(n, dtype=torch.uint8, device=w_router.device)
+    check(_lib().moe_router_split(ctypes.byref(cfg), _ptr(w_router), _ptr(out), out.numel(),
                                   _stream(stream)))
     return out
 
@@ -341,7 +343,12 @@ class MoELayer:
         self.resplit_router()
 
     def resplit_router(self, stream=None) -> None:
-        self.w_router_split = router_split(self.cfg, self.w_router, stream)
+        """Split the router weight again, into the buffer of the split before: captured forwards
+        read that one.  Order it with the forwards before and after, as the change of w_router."""
+        split = getattr(self, "w_router_split", None)
+        if split is not None and split.numel() != router_split_size(self.cfg):
+            split = None
+        self.w_router_split = router_split(self.cfg, self.w_router, stream, split)
 
     def inputs(self, x) -> MoeLayerInputs:
         b = self.logit_bias

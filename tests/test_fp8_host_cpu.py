@@ -23,6 +23,7 @@ class FakeLibrary:
         self.status, self.calls, self.last = {}, [], b""
         self.device = 0  # the current device, as torch.cuda.device sets it
         self.streams = [1000, 1001]  # each device's current stream
+        self.split_bytes = 4096
 
     def moe_check_device_error(self, ws, n, stream):
         self.calls.append(("check", ws, self.device, stream))
@@ -39,7 +40,7 @@ class FakeLibrary:
         return self.last
 
     def moe_router_split_size(self, cfg, n):
-        ctypes.cast(n, ctypes.POINTER(ctypes.c_size_t))[0] = 4096
+        ctypes.cast(n, ctypes.POINTER(ctypes.c_size_t))[0] = self.split_bytes
         return 0
 
     def moe_router_split(self, cfg, w, out, n, stream):
@@ -253,3 +254,17 @@ def test_weights_on_the_host_are_refused():
     w = torch.zeros(1, 16, 16)
     with pytest.raises(ValueError):
         M.Fp8Experts.quantize(w, w, w)
+
+
+def test_a_router_weight_is_split_again_where_it_was(lib):
+    """A captured forward reads the split router weight at the address it had then."""
+    layer = bare_layer(1)
+    layer.resplit_router()
+    first = layer.w_router_split
+    layer.resplit_router()
+    layer.resplit_router(77)
+    assert layer.w_router_split is first
+    assert lib.calls == [("split", first.address, 1, 1001)] * 2 + [("split", first.address, 1, 77)]
+    layer.cfg.d_model, lib.split_bytes = 512, 8192  # another layer's router weight: another buffer
+    layer.resplit_router()
+    assert layer.w_router_split.numel() == 8192

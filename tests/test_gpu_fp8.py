@@ -819,3 +819,33 @@ def test_check_restores_the_workspace_whatever_the_errors(layer_code, code):
     assert not words.any()
     assert torch.equal(layer(inp.x), want)
     layer.check_device_error()
+
+
+@pytest.mark.parametrize("kind", ["fp8", "bf16"])
+def test_router_weight_changed_under_a_captured_forward(kind):
+    """The graph routes by the router weight as resplit_router last split it, other tensors having
+    come and gone in between."""
+    shape = W.reduced(W.DSV3_DECODE, 64, 256, 128)
+    inp = W.make_inputs(shape, device="cuda")
+    cfg = M.config_from_shape(shape)
+    assert M.router_split_size(cfg) > 0
+
+    def layer_of(w_router):
+        if kind == "bf16":
+            return M.MoELayer(cfg, w_router, inp.w_gate, inp.w_up, inp.w_down, inp.logit_bias)
+        return M.MoELayerFp8(cfg, w_router, M.Fp8Experts.quantize(inp.w_gate, inp.w_up, inp.w_down),
+                             inp.logit_bias)
+
+    w_router = inp.w_router.clone()
+    layer = layer_of(w_router)
+    graph = layer.capture(inp.x)
+    graph.replay()
+    before = layer.bufs.out.clone()
+    w_router.copy_(inp.w_router.flip(1))
+    layer.resplit_router()
+    size = M.router_split_size(cfg)
+    junk = [torch.full((size,), 0x5A, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    graph.replay()
+    got = layer.bufs.out.clone()
+    assert torch.equal(got, layer_of(w_router)(inp.x)) and not torch.equal(got, before)
+    del junk

@@ -605,7 +605,8 @@ moe_status_t moe_fp8_workspace_init(void* ws, size_t ws_bytes, void* stream);
  * a plain product).  Rows outside every bucket are neither read nor written; buckets must not
  * overlap.  A bucket that reaches outside [0, rows) is skipped and reported by
  * moe_check_device_error as MOE_ERR_DEVICE_DATA.  N is a multiple of 8.  rows = 0 does
- * nothing.  The order of every sum is fixed by the sizes and the buckets: equal inputs give
+ * nothing; more than 2^31 - 128 rows, or tiles of 128 x 128 entries beyond 2^31 - 2^16, are
+ * MOE_ERR_UNSUPPORTED (moe_expert_ffn_fp8 too, of max_rows).  The order of every sum is fixed by the sizes and the buckets: equal inputs give
  * equal bits.
  */
 moe_status_t moe_fp8_grouped_gemm(int32_t E, int64_t rows, int64_t N, int64_t K, const void* a_q,

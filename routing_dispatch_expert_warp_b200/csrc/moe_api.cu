@@ -934,10 +934,12 @@ moe_status_t check_fp8_ws(const char* name, const void* ws, size_t ws_bytes) {
   return MOE_OK;
 }
 
-// Tiles are numbered in 32 bits.
+// Rows and tiles are numbered in 32 bits.
 moe_status_t check_fp8_tiles(const char* name, int64_t E, int64_t rows, int64_t N) {
-  if ((rows / 128 + E) * ((N + 127) / 128) > 2147483647LL)
-    return fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^31 output tiles", name);
+  if (rows > kFp8MaxRows)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^31 - 128 rows", name);
+  if ((rows / 128 + E) * ((N + 127) / 128) > kFp8MaxTiles)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^31 - 2^16 output tiles", name);
   return MOE_OK;
 }
 

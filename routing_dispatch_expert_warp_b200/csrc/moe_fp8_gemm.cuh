@@ -13,7 +13,7 @@ struct Fp8Params {
   const int32_t* seg_start;  // [E] first row of each bucket
   const int32_t* seg_count;  // [E] rows of each bucket
   int E;
-  int64_t rows;        // rows of a, a_scale and the outputs
+  int64_t rows;        // rows of a, a_scale and the outputs (at most kFp8MaxRows)
   int K;               // reduction length (a multiple of 16)
   int N;               // output columns (LINEAR a multiple of 8, GATED of 16)
   int n_blocks;        // tiles along the output columns
@@ -175,7 +175,7 @@ __device__ void build_buckets(Buckets& t, const Fp8Params& p, int lane) {
         c = 0;
       }
       t.start[e] = s;
-      t.count[e] = c;
+      t.count[e] = c;  // (at most kFp8MaxRows: the next sum fits)
       mb = (c + ROWS - 1) / ROWS;
     }
     int v = mb;
@@ -188,7 +188,7 @@ __device__ void build_buckets(Buckets& t, const Fp8Params& p, int lane) {
     carry += __shfl_sync(0xffffffffu, v, 31);
   }
   // (only buckets that overlap can have more tiles than an int counts: then none is taken)
-  const bool fits = carry * p.n_blocks <= 2147483647;
+  const bool fits = carry * p.n_blocks <= kFp8MaxTiles;
   if (!fits && blockIdx.x == 0)
     record_error(p.status, DEV_BAD_BUCKET, 40, static_cast<unsigned long long>(p.E - 1));
   if (lane == 0) t.tile_base[p.E] = fits ? static_cast<int>(carry) * p.n_blocks : 0;

@@ -189,6 +189,10 @@ struct Fp8Gemm {
   bool follows;             // the launch before in the stream is the product that made a: only
                             // a and a_scale depend on it
 };
+// Most rows of a product: rounded up to whole tiles of 128 they still fit in an int.
+constexpr int64_t kFp8MaxRows = 2147483647LL - 127;
+// Most tiles of a product: so does a block's step past the last one.
+constexpr int64_t kFp8MaxTiles = 2147483647LL - 65535;
 // Workspace of the fp8 products: the status record, then arrival counters (zero between
 // calls), then partial sums.
 constexpr size_t kFp8CountersOffset = 256;

@@ -299,3 +299,36 @@ def test_oracle_products_and_blocks():
         for k in (0, 130, 271):
             m = w[0, n // 128 * 128:n // 128 * 128 + 128, k // 128 * 128:k // 128 * 128 + 128]
             assert s[0, n // 128, k // 128] == np.float32(m.abs().max()) / np.float32(448)
+
+
+# ------------------------------------------------------------------ the largest sizes
+def test_rows_that_tiles_cannot_number_are_refused(lib):
+    """Rows are rounded up to whole tiles in 32 bits: 2^31 - 128 is the most that they can be."""
+    n = ws_bytes(lib)
+
+    def gemm(rows, a=P):
+        return lib.moe_fp8_grouped_gemm(1, rows, 8, 16, a, P, P, P, P, P, P, P, n, None)
+
+    for rows in range(2 ** 31 - 127, 2 ** 31):
+        assert gemm(rows) == UNSUPPORTED, rows
+    assert gemm(2 ** 31 - 128, a=None) == INVALID  # as far as the pointers
+
+    def ffn(T, x=P):
+        cfg = M.make_config(T, 16, 16, 1, 1)
+        return lib.moe_expert_ffn_fp8(ctypes.byref(cfg), x, P, P, P, ctypes.byref(experts_struct()),
+                                      P, P, P, P, n, None)
+
+    assert ffn(2 ** 31 - 1) == ffn(2 ** 31 - 127) == UNSUPPORTED
+    assert ffn(2 ** 31 - 128, x=None) == INVALID
+
+
+def test_tiles_that_32_bits_cannot_number_are_refused(lib):
+    """A block steps from tile to tile in 32 bits: the step past the last one must fit too."""
+    n = ws_bytes(lib)
+
+    def gemm(rows, N, a=P):
+        return lib.moe_fp8_grouped_gemm(1, rows, N, 16, a, P, P, P, P, P, P, P, n, None)
+
+    # (rows / 128 + 1) x 128 tiles of 128 x 128
+    assert gemm(128 * (2 ** 24 - 2), 128 * 128) == UNSUPPORTED
+    assert gemm(128 * (2 ** 24 - 1024), 128 * 128, a=None) == INVALID

@@ -849,3 +849,26 @@ def test_router_weight_changed_under_a_captured_forward(kind):
     got = layer.bufs.out.clone()
     assert torch.equal(got, layer_of(w_router)(inp.x)) and not torch.equal(got, before)
     del junk
+
+
+def test_grouped_gemm_of_the_most_rows():
+    """2^31 - 128 rows, the most that are taken: whole tiles up to the last row."""
+    rows, K, N = 2 ** 31 - 128, 16, 8
+    if torch.cuda.mem_get_info()[0] < 100 * 2 ** 30:
+        pytest.skip("needs 100 GB of free device memory")
+    g = gen(9)
+    a_q = torch.zeros((rows, K), dtype=torch.uint8, device="cuda").view(E4M3)
+    a_s = torch.zeros((rows, 1), device="cuda")
+    last_q, last_s = quantized_rows(torch.randn((300, K), generator=g))
+    a_q.view(torch.uint8)[-300:] = last_q.view(torch.uint8)
+    a_s[-300:] = last_s
+    w_q, w_s = quantized_weights(torch.randn((1, N, K), generator=g))
+    out = torch.full((rows, N), 3.25, dtype=torch.bfloat16, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ws = M.alloc_fp8_workspace()
+    M.moe_fp8_grouped_gemm(a_q, a_s, torch.zeros(1, **i32), torch.full((1,), rows, **i32), w_q, w_s,
+                           out, ws)
+    M.moe_check_device_error(ws)
+    check_product(out[-300:], last_q, last_s, w_q, w_s, [0], [300])
+    for at in (0, 2 ** 30, 2 ** 31 - 1000):
+        assert not out[at:at + 500].any()

@@ -62,8 +62,8 @@ constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int CTRL_WARPS = 4;
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 32 * (CTRL_WARPS + EPI_WARPS);
-// The launch's 168 registers a thread are split anew: 128 x 72 + 256 x 216 = 384 x 168.  (The
-// split stands at the head of each role's branch: the compiler goes by it there.)
+// The launch's 168 registers a thread are split anew: 128 x 72 + 256 x 216 = 384 x 168.  All warps
+// of a warpgroup have to execute the same setmaxnreg: the four control warps do before they part.
 constexpr int LAUNCH_REGS = 168, CTRL_REGS = 72, EPI_REGS = 216;
 static_assert(32 * (CTRL_WARPS * CTRL_REGS + EPI_WARPS * EPI_REGS) <= THREADS * LAUNCH_REGS,
               "setmaxnreg.inc would wait for registers that the block does not have");
@@ -196,150 +196,150 @@ __global__ void __launch_bounds__(THREADS, 1) fp8_grouped_gemm_kernel(
     return true;
   };
 
-  if (warp == 0) {
-    // ---------------------------------------------------------------- TMA producer
+  if (warp < CTRL_WARPS) {
     regs_dec<CTRL_REGS>();
-    uint32_t fills = 0;  // bit s: parity of stage s's next fill
-    uint32_t armed = 0, armed_parity = 0;
-    bool ok = true, waited = false;
-    int early = 0;  // blocks of the first tile whose weights were loaded ahead
-    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-      const Tile t = decode<BM>(bk, p, tile);
-      const int groups = t.valid > BM - 32 ? BM / 32 : (t.valid + 31) >> 5;  // of 32 rows
-      auto load_weights = [&](int kb) {
-        const int s = kb & (STAGES - 1);
-        uint8_t* sb = smem + s * STAGE_BYTES + A_BYTES;
-        mbar_arrive_expect_tx(&full_bar[s], B_BYTES + groups * 32 * BK);
-        if (GATED) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint8_t* to = sb + h * HALF_N * BK;
-            tma_load_3d(to, &tm_b0, &full_bar[s], kb * BK, t.nb * 128 + h * 64, t.e);
-            tma_load_3d(to + 64 * BK, &tm_b1, &full_bar[s], kb * BK, t.nb * 128 + h * 64, t.e);
-          }
-        } else {
-          tma_load_3d(sb, &tm_b0, &full_bar[s], kb * BK, t.nb * BN, t.e);
-        }
-      };
-      if (!waited) {  // when it follows, the first blocks' weights do not depend on the other
-        early = min(STAGES, KB);
-        if (elect_one())
-          for (int kb = 0; kb < early; ++kb) load_weights(kb);
-        __syncwarp();
-        wait_for_previous();
-        waited = true;
-      }
-#pragma unroll 1
-      for (int kb = 0; kb < KB; ++kb) {
-        const int s = kb & (STAGES - 1);
-        const uint32_t par = (fills >> s) & 1u;
-        const bool ahead = early > 0;
-        if (!ahead && (!await(&done_bar[0][s], par ^ 1u, 41, tile) ||
-                       !await(&done_bar[1][s], par ^ 1u, 41, tile))) {
-          ok = false;
-          break;
-        }
-        uint8_t* sa = smem + s * STAGE_BYTES;
-        if (elect_one()) {
-          if (!ahead) load_weights(kb);
-          if (groups == 4) {
-            tma_load_2d(sa, &tm_a, &full_bar[s], kb * BK, t.row0);
+    if (warp == 0) {
+      // ---------------------------------------------------------------- TMA producer
+      uint32_t fills = 0;  // bit s: parity of stage s's next fill
+      uint32_t armed = 0, armed_parity = 0;
+      bool ok = true, waited = false;
+      int early = 0;  // blocks of the first tile whose weights were loaded ahead
+      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+        const Tile t = decode<BM>(bk, p, tile);
+        const int groups = t.valid > BM - 32 ? BM / 32 : (t.valid + 31) >> 5;  // of 32 rows
+        auto load_weights = [&](int kb) {
+          const int s = kb & (STAGES - 1);
+          uint8_t* sb = smem + s * STAGE_BYTES + A_BYTES;
+          mbar_arrive_expect_tx(&full_bar[s], B_BYTES + groups * 32 * BK);
+          if (GATED) {
+  #pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint8_t* to = sb + h * HALF_N * BK;
+              tma_load_3d(to, &tm_b0, &full_bar[s], kb * BK, t.nb * 128 + h * 64, t.e);
+              tma_load_3d(to + 64 * BK, &tm_b1, &full_bar[s], kb * BK, t.nb * 128 + h * 64, t.e);
+            }
           } else {
-            for (int g = 0; g < groups; ++g)
-              tma_load_2d(sa + g * 32 * BK, &tm_a32, &full_bar[s], kb * BK, t.row0 + g * 32);
+            tma_load_3d(sb, &tm_b0, &full_bar[s], kb * BK, t.nb * BN, t.e);
           }
+        };
+        if (!waited) {  // when it follows, the first blocks' weights do not depend on the other
+          early = min(STAGES, KB);
+          if (elect_one())
+            for (int kb = 0; kb < early; ++kb) load_weights(kb);
+          __syncwarp();
+          wait_for_previous();
+          waited = true;
         }
-        __syncwarp();
-        if (ahead) --early;
-        armed |= 1u << s;
-        armed_parity = (armed_parity & ~(1u << s)) | (par << s);
-        fills ^= 1u << s;
+  #pragma unroll 1
+        for (int kb = 0; kb < KB; ++kb) {
+          const int s = kb & (STAGES - 1);
+          const uint32_t par = (fills >> s) & 1u;
+          const bool ahead = early > 0;
+          if (!ahead && (!await(&done_bar[0][s], par ^ 1u, 41, tile) ||
+                         !await(&done_bar[1][s], par ^ 1u, 41, tile))) {
+            ok = false;
+            break;
+          }
+          uint8_t* sa = smem + s * STAGE_BYTES;
+          if (elect_one()) {
+            if (!ahead) load_weights(kb);
+            if (groups == 4) {
+              tma_load_2d(sa, &tm_a, &full_bar[s], kb * BK, t.row0);
+            } else {
+              for (int g = 0; g < groups; ++g)
+                tma_load_2d(sa + g * 32 * BK, &tm_a32, &full_bar[s], kb * BK, t.row0 + g * 32);
+            }
+          }
+          __syncwarp();
+          if (ahead) --early;
+          armed |= 1u << s;
+          armed_parity = (armed_parity & ~(1u << s)) | (par << s);
+          fills ^= 1u << s;
+        }
       }
-    }
-    if (!waited) wait_for_previous();
-    // every fill must land before the block can exit
-    for (int s = 0; s < STAGES; ++s)
-      if ((armed >> s) & 1u)
-        mbar_wait(&full_bar[s], (armed_parity >> s) & 1u, kDrainNs, nullptr);
-    __syncwarp();
-  } else if (warp < 3) {
-    // ---------------------------------------------------------------- MMA issuers
-    regs_dec<CTRL_REGS>();
-    wait_for_previous();
-    constexpr uint32_t idesc = idesc_e4m3_f32(BM, HALF_N);
-    const int h = warp - 1;
-    const uint64_t a_desc = sw128_kmajor_desc(smem_addr(smem));
-    const uint64_t b_desc = sw128_kmajor_desc(smem_addr(smem) + A_BYTES + h * HALF_N * BK);
-    uint32_t fills = 0, uses = 0;  // parities: stage s's next fill, accumulator j's next use
-    bool ok = true, issued = false;
-    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-#pragma unroll 4
-      for (int kb = 0; kb < KB; ++kb) {
-        const int s = kb & (STAGES - 1), j = kb & 1;
-        if (!await(&full_bar[s], (fills >> s) & 1u, 42, tile) ||
-            !await(&tempty_bar[h][j], ((uses >> j) & 1u) ^ 1u, 42, tile)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t d_tmem = tmem_base + static_cast<uint32_t>((2 * h + j) * HALF_N);
-#pragma unroll
-          for (int kk = 0; kk < BK / 32; ++kk)  // descriptors count 16-byte units
-            tc_mma_e4m3(d_tmem, a_desc + (s * STAGE_BYTES + kk * 32) / 16,
-                        b_desc + (s * STAGE_BYTES + kk * 32) / 16, idesc, kk != 0 ? 1u : 0u);
-          tc_commit(&done_bar[h][s]);
-        }
-        __syncwarp();
-        issued = true;
-        fills ^= 1u << s;
-        uses ^= 1u << j;
-      }
-    }
-    if (!ok && issued) {  // MMAs still reading smem / writing TMEM must finish first
-      if (elect_one()) tc_commit(&drain_bar[h]);
-      mbar_wait(&drain_bar[h], 0, kDrainNs, nullptr);
+      if (!waited) wait_for_previous();
+      // every fill must land before the block can exit
+      for (int s = 0; s < STAGES; ++s)
+        if ((armed >> s) & 1u)
+          mbar_wait(&full_bar[s], (armed_parity >> s) & 1u, kDrainNs, nullptr);
       __syncwarp();
-    }
-  } else if (warp == 3) {
-    // ---------------------------------------------------------------- scales
-    regs_dec<CTRL_REGS>();
-    wait_for_previous();
-    // A lane has rows lane + 32 i of the tile.  (The epilogue's threads loading their own rows'
-    // scales took a fifth of its time: 32 rows' lanes are 32 passes of the L1.)
-    uint32_t turns = 0;  // of 4 blocks, over all tiles
-    bool ok = true;
-    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-      const Tile t = decode<BM>(bk, p, tile);
-      const float* sa = p.a_scale + (static_cast<int64_t>(t.row0) + lane) * KB;
-      const int64_t w_row = static_cast<int64_t>(t.e) * p.nsb;
-      // LINEAR: the two halves' blocks of columns (one past the last is never stored)
-      const float* s0 = p.w_scale0 + (w_row + (GATED ? t.nb : 2 * t.nb)) * KB;
-      const float* s1 = GATED ? p.w_scale1 + (w_row + t.nb) * KB
-                              : p.w_scale0 + (w_row + min(2 * t.nb + 1, p.nsb - 1)) * KB;
-      for (int k0 = 0; k0 < KB; k0 += 4) {
-        float4 a[4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-          a[m] = lane + 32 * m < t.valid
-                     ? scales4(sa + static_cast<int64_t>(32 * m) * KB, k0, KB)
-                     : make_float4(0.f, 0.f, 0.f, 0.f);
-        const float4 w0 = scales4(s0, k0, KB), w1 = scales4(s1, k0, KB);
-        const uint32_t b = turns & 1u;
-        if (!await(&sfree_bar[b], ((turns >> 1) & 1u) ^ 1u, 45, tile)) {
-          ok = false;
-          break;
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            scale_s[b][k][0][lane + 32 * m] = pick(a[m], k) * pick(w0, k);
-            scale_s[b][k][1][lane + 32 * m] = pick(a[m], k) * pick(w1, k);
+    } else if (warp < 3) {
+      // ---------------------------------------------------------------- MMA issuers
+      wait_for_previous();
+      constexpr uint32_t idesc = idesc_e4m3_f32(BM, HALF_N);
+      const int h = warp - 1;
+      const uint64_t a_desc = sw128_kmajor_desc(smem_addr(smem));
+      const uint64_t b_desc = sw128_kmajor_desc(smem_addr(smem) + A_BYTES + h * HALF_N * BK);
+      uint32_t fills = 0, uses = 0;  // parities: stage s's next fill, accumulator j's next use
+      bool ok = true, issued = false;
+      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+  #pragma unroll 4
+        for (int kb = 0; kb < KB; ++kb) {
+          const int s = kb & (STAGES - 1), j = kb & 1;
+          if (!await(&full_bar[s], (fills >> s) & 1u, 42, tile) ||
+              !await(&tempty_bar[h][j], ((uses >> j) & 1u) ^ 1u, 42, tile)) {
+            ok = false;
+            break;
           }
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t d_tmem = tmem_base + static_cast<uint32_t>((2 * h + j) * HALF_N);
+  #pragma unroll
+            for (int kk = 0; kk < BK / 32; ++kk)  // descriptors count 16-byte units
+              tc_mma_e4m3(d_tmem, a_desc + (s * STAGE_BYTES + kk * 32) / 16,
+                          b_desc + (s * STAGE_BYTES + kk * 32) / 16, idesc, kk != 0 ? 1u : 0u);
+            tc_commit(&done_bar[h][s]);
+          }
+          __syncwarp();
+          issued = true;
+          fills ^= 1u << s;
+          uses ^= 1u << j;
+        }
+      }
+      if (!ok && issued) {  // MMAs still reading smem / writing TMEM must finish first
+        if (elect_one()) tc_commit(&drain_bar[h]);
+        mbar_wait(&drain_bar[h], 0, kDrainNs, nullptr);
         __syncwarp();
-        arrive_if(&sfull_bar[b], lane == 0);
-        ++turns;
+      }
+    } else if (warp == 3) {
+      // ---------------------------------------------------------------- scales
+      wait_for_previous();
+      // A lane has rows lane + 32 i of the tile.  (The epilogue's threads loading their own rows'
+      // scales took a fifth of its time: 32 rows' lanes are 32 passes of the L1.)
+      uint32_t turns = 0;  // of 4 blocks, over all tiles
+      bool ok = true;
+      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+        const Tile t = decode<BM>(bk, p, tile);
+        const float* sa = p.a_scale + (static_cast<int64_t>(t.row0) + lane) * KB;
+        const int64_t w_row = static_cast<int64_t>(t.e) * p.nsb;
+        // LINEAR: the two halves' blocks of columns (one past the last is never stored)
+        const float* s0 = p.w_scale0 + (w_row + (GATED ? t.nb : 2 * t.nb)) * KB;
+        const float* s1 = GATED ? p.w_scale1 + (w_row + t.nb) * KB
+                                : p.w_scale0 + (w_row + min(2 * t.nb + 1, p.nsb - 1)) * KB;
+        for (int k0 = 0; k0 < KB; k0 += 4) {
+          float4 a[4];
+  #pragma unroll
+          for (int m = 0; m < 4; ++m)
+            a[m] = lane + 32 * m < t.valid
+                       ? scales4(sa + static_cast<int64_t>(32 * m) * KB, k0, KB)
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
+          const float4 w0 = scales4(s0, k0, KB), w1 = scales4(s1, k0, KB);
+          const uint32_t b = turns & 1u;
+          if (!await(&sfree_bar[b], ((turns >> 1) & 1u) ^ 1u, 45, tile)) {
+            ok = false;
+            break;
+          }
+  #pragma unroll
+          for (int k = 0; k < 4; ++k)
+  #pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              scale_s[b][k][0][lane + 32 * m] = pick(a[m], k) * pick(w0, k);
+              scale_s[b][k][1][lane + 32 * m] = pick(a[m], k) * pick(w1, k);
+            }
+          __syncwarp();
+          arrive_if(&sfull_bar[b], lane == 0);
+          ++turns;
+        }
       }
     }
   } else {

@@ -2,6 +2,8 @@
 in these tests), the struct mirrors, and the 64-bit oracle's own arithmetic."""
 import ctypes
 import fractions
+import os
+import re
 import subprocess
 
 import numpy as np
@@ -332,3 +334,22 @@ def test_tiles_that_32_bits_cannot_number_are_refused(lib):
     # (rows / 128 + 1) x 128 tiles of 128 x 128
     assert gemm(128 * (2 ** 24 - 2), 128 * 128) == UNSUPPORTED
     assert gemm(128 * (2 ** 24 - 1024), 128 * 128, a=None) == INVALID
+
+
+# ------------------------------------------------------------------ the kernels' source
+def test_a_warpgroup_has_one_register_split():
+    """All warps of a warpgroup have to execute the same setmaxnreg: a kernel says it once for the
+    four control warps, before they part, and once for the epilogue's."""
+    seen = 0
+    for name in sorted(os.listdir(B.CSRC)):
+        with open(os.path.join(B.CSRC, name)) as f:
+            text = re.sub(r"//[^\n]*", "", f.read())
+        if "setmaxnreg" not in text:
+            continue
+        seen += 1
+        assert text.count('("setmaxnreg.dec') == text.count('("setmaxnreg.inc') == 1, name
+        assert len(re.findall(r"if \(warp < CTRL_WARPS\) \{\s*regs_dec<\w+>\(\);", text)) == 1, name
+        assert len(re.findall(r"regs_dec<\w+>\(\)", text)) == 1, name
+        assert len(re.findall(r"\} else \{\s*regs_inc<\w+>\(\);", text)) == 1, name
+        assert len(re.findall(r"regs_inc<\w+>\(\)", text)) == 1, name
+    assert seen == 1

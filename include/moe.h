@@ -602,12 +602,19 @@ moe_status_t moe_fp8_workspace_init(void* ws, size_t ws_bytes, void* stream);
  *               (sum over c in block b of a_q[r, c] * w_q[e, n, c])
  * summed in fp32, out [rows, N] bf16.  a_q [rows, K], w_q [E, N, K]; seg_start, seg_count [E]
  * int32 device arrays (moe_dispatch's expert_offsets and kept_counts, or any others; E = 1 is
- * a plain product).  Rows outside every bucket are neither read nor written; buckets must not
- * overlap.  A bucket that reaches outside [0, rows) is skipped and reported by
- * moe_check_device_error as MOE_ERR_DEVICE_DATA.  N is a multiple of 8.  rows = 0 does
- * nothing; more than 2^31 - 128 rows, or tiles of 128 x 128 entries beyond 2^31 - 2^16, are
- * MOE_ERR_UNSUPPORTED (moe_expert_ffn_fp8 too, of max_rows).  The order of every sum is fixed by the sizes and the buckets: equal inputs give
- * equal bits.
+ * a plain product).  Rows outside every bucket are not written and have no part in any result,
+ * whatever they hold (a load may bring in those next to a bucket); buckets must not overlap.  A
+ * bucket that reaches outside [0, rows) is skipped and reported by moe_check_device_error as
+ * MOE_ERR_DEVICE_DATA.  N is a multiple of 8.  rows = 0 does nothing; more than 2^31 - 128 rows,
+ * or tiles of 128 x 128 entries beyond 2^31 - 2^16, are MOE_ERR_UNSUPPORTED (moe_expert_ffn_fp8
+ * too, of max_rows).
+ *   The two scales of a block are multiplied first, in fp32: where that product is below 2^-126 a
+ * block adds an error of at most 2^-125, where it is 2^128 or more the entry is infinite or NaN.
+ *   `rows`, the length of the buffers, also chooses the kernel, since the host does not know the
+ * buckets: up to 32 rows an expert one with tiles of 64 rows that is bound by reading the
+ * weights, above it one with tiles of 128 rows.  Either is right for any buckets; buffers with much
+ * more rows than the buckets have, as in a padded layout, give a decode step the second one.
+ *   The order of every sum is fixed by the sizes and the buckets: equal inputs give equal bits.
  */
 moe_status_t moe_fp8_grouped_gemm(int32_t E, int64_t rows, int64_t N, int64_t K, const void* a_q,
                                   const float* a_scale, const int32_t* seg_start,
@@ -631,8 +638,10 @@ typedef struct moe_fp8_experts {
  *   h = silu(x[r] . w_gate[e]^T) * (x[r] . w_up[e]^T)  in fp32, then quantised as a row:
  *   h_q [max_rows, d_ff] e4m3, h_scale [max_rows, ceil(d_ff / 128)] fp32
  *   y_perm[r, :] = h[r] . w_down[e]^T                   [max_rows, d_model] bf16
- * products as in moe_fp8_grouped_gemm.  Here 448 h / m is rounded to fp32 before it is
- * rounded to e4m3 (h itself is an fp32 sum).  bf16 layers only (MOE_ERR_UNSUPPORTED
+ * products as in moe_fp8_grouped_gemm (its `rows` is max_rows).  Here q is the e4m3 number nearest
+ * to fp32(h * fp32(448 / m)): two roundings to fp32 before the one to e4m3 (h itself is an fp32
+ * sum).  silu's exp is off by up to 2 + 1.2 |gate| units of the last place of fp32; below a gate of
+ * -87.3 silu is 0, its magnitude being less than 2^-119.  bf16 layers only (MOE_ERR_UNSUPPORTED
  * otherwise).  x_q, x_scale: moe_fp8_permute_rows' outputs.
  */
 moe_status_t moe_expert_ffn_fp8(const moe_config_t* cfg, const void* x_q, const float* x_scale,

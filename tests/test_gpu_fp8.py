@@ -874,3 +874,87 @@ def test_grouped_gemm_of_the_most_rows():
         assert not out[at:at + 500].any()
     del a_q, a_s, out
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("slack", [0, 200], ids=["few-rows kernel", "many-rows kernel"])
+@pytest.mark.parametrize("counts", [[32] * 8, [33, 0, 1, 64, 2, 0, 100, 56], [64, 0, 0, 64],
+                                    [48, 0], [0, 0, 0, 65, 0, 0, 0, 63]])
+def test_the_same_buckets_in_either_kernel(counts, slack):
+    """The length of the buffers chooses the kernel; the buckets are the same.  What lies behind
+    them, NaN here, has no part in the results."""
+    N, K, E = 520, 1040, len(counts)
+    first, used = starts(counts)
+    rows = used if slack == 0 else 32 * E + slack
+    a_q, a_s = quantized_rows(torch.randn((rows, K), generator=gen(3)).bfloat16())
+    a_q.view(torch.uint8)[used:] = 0x7F
+    a_s[used:] = float("nan")
+    w_q, w_s = quantized_weights(torch.randn((E, N, K), generator=gen(4)) / K ** 0.5)
+    out = torch.full((rows, N), 3.25, dtype=torch.bfloat16, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ws = M.alloc_fp8_workspace()
+    M.moe_fp8_grouped_gemm(a_q, a_s, torch.tensor(first, **i32), torch.tensor(counts, **i32), w_q,
+                           w_s, out, ws)
+    M.moe_check_device_error(ws)
+    check_product(out, a_q, a_s, w_q, w_s, first, counts)
+
+
+@pytest.mark.parametrize("rows", [5, 40], ids=["few", "many"])
+def test_scale_products_below_the_smallest_normal_number(rows):
+    """a_scale w_scale is rounded to a multiple of 2^-149 there, off by at most 2^-150; a block's
+    sum is at most 128 x 448^2 < 2^24.7, so a block adds at most 2^-125 to the error."""
+    N, K = 136, 400
+    g = gen(8)
+    a = torch.randint(0, 256, (rows, K), generator=g, dtype=torch.uint8)
+    w = torch.randint(0, 256, (1, N, K), generator=g, dtype=torch.uint8)
+    for t in (a, w):
+        t[(t & 0x7F) == 0x7F] = 0x7E  # (no NaN)
+    a, w = a.cuda().view(E4M3), w.cuda().view(E4M3)
+    a_s = torch.exp2(-80 - 20 * torch.rand((rows, 4), generator=g)).cuda()
+    w_s = torch.exp2(-55 - 10 * torch.rand((1, 2, 4), generator=g)).cuda()
+    out = torch.full((rows, N), 3.25, dtype=torch.bfloat16, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    M.moe_fp8_grouped_gemm(a, a_s, torch.zeros(1, **i32), torch.full((1,), rows, **i32), w, w_s,
+                           out, M.alloc_fp8_workspace())
+    ref, mag = O.product(O.rows_value(a, a_s), O.weight_value(w[0], w_s[0]))
+    assert (ref.abs() < 2.0 ** -105).all() and (ref.abs() > 2.0 ** -126).any()
+    # bf16 rounds to multiples of 2^-133 below its smallest normal number
+    room = (1 + O.BF16_HALF_STEP) * (O.sum_error(K) * mag + 4 * 2.0 ** -125)
+    room = room + torch.clamp(O.BF16_HALF_STEP * ref.abs(), min=2.0 ** -134)
+    assert ((out.cpu().double() - ref).abs() <= room).all()
+
+
+@pytest.mark.parametrize("times", [1, 3], ids=["few", "many"])
+def test_silu_of_far_gates(times):
+    """Gates from -1000 to 1000, one to a row, times an up of 1: below -87.3 silu is 0, off by less
+    than 2^-119."""
+    gates = [-1000.0, -448.0, -104.0, -96.0, -90.0, -88.0, -87.5, -87.0, -80.0, -20.0, -1.0, -2e-3,
+             0.0, 2e-3, 1.0, 20.0, 88.0, 100.0, 1000.0] * times
+    R, d, f = len(gates), 256, 16
+    x = torch.zeros((R, d))
+    x[:, 0] = torch.tensor(gates)
+    x[:, 128] = 1.0
+    wg, wu = torch.zeros((1, f, d)), torch.zeros((1, f, d))
+    wg[:, :, 0], wu[:, :, 128] = 1.0, 1.0
+    x_q, x_s = quantized_rows(x)
+    experts = M.Fp8Experts.quantize(wg.cuda(), wu.cuda(), torch.ones((1, d, f), device="cuda"))
+    cfg = M.make_config(R, d, f, 1, 1)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    h_q, h_s = torch.empty((R, f), device="cuda").to(E4M3), torch.empty((R, 1), device="cuda")
+    y = torch.empty((R, d), dtype=torch.bfloat16, device="cuda")
+    M.moe_expert_ffn_fp8(cfg, x_q, x_s, torch.tensor([0, R], **i32), torch.full((1,), R, **i32),
+                         experts, h_q, h_s, y, M.alloc_fp8_workspace())
+    v = O.rows_value(x_q, x_s)
+    g = O.product(v, O.weight_value(experts.w_gate[0], experts.gate_scale[0]))[0]
+    u = O.product(v, O.weight_value(experts.w_up[0], experts.up_scale[0]))[0]
+    ref = g * torch.sigmoid(g) * u
+    # Gate and up have one product each: two roundings of 2^-24, and silu moves by at most 1 + |g|
+    # of itself for as much of g.  The fast exp of -g is off by up to 2 + 1.2 |g| units of 2^-23.  32
+    # steps for the division and the products, as in test_ffn.
+    room = (2 * (1 + g.abs()) + 2 + 2 * (2 + 1.2 * g.abs()) + 32) * 2.0 ** -24 * ref.abs()
+    room = room + 2.0 ** -119 * u.abs()
+    # the entries of a row are alike: its scale is |h| / 448, or that of 2^-100
+    step = torch.maximum(O.E4M3_HALF_STEP * ref.abs(), torch.tensor(2.0 ** -110 / 448).double())
+    step[ref.abs() > 2.0 ** -99] = 0.0  # q = 448: the largest entry maps to itself
+    off = (O.rows_value(h_q, h_s) - ref).abs()
+    assert (off <= room + (1 + 2.0 ** -15) * step).all(), (off / (room + step)).max()
+    assert (O.rows_value(h_q, h_s)[:3] == 0).all()

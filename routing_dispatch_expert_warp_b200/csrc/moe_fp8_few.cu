@@ -2,11 +2,11 @@
 // places.  A tile is 256 weight rows x up to 64 bucket rows; the weight rows are the MMA's 128
 // rows twice over (two halves), the bucket rows its N = 16 .. 64 columns, taken in steps of 16.
 // What bounds such a product is reading each expert's weight once.  With the rows in the MMA's
-// 128 places, 4 rows cost the tensor cores and the epilogue as much as 128 (and power, which
-// the clocks pay for): a DeepSeek-shaped decode step of 4 rows an expert takes 2.08 ms there and
-// 1.60 to 1.66 here, where a block of 128 costs the epilogue 16 sums a thread; that is 6.6 to 6.9
-// TB/s.  32 experts of 7168 x 2048 with 128 rows take 78 us, 6.0 TB/s; one token through the
-// Mixtral-8x7B shaped experts 67, of which reading the weights is 54.
+// 128 places, 4 rows cost the tensor cores and the epilogue as much as 128 (and power, which the
+// clocks pay for): a DeepSeek-shaped decode step of 4 rows an expert takes 2.08 ms there and 1.60
+// to 1.68 here, where a block of 128 costs the epilogue 16 sums a thread; that is 6.6 to 6.9
+// TB/s.  32 experts of 7168 x 2048 with 128 rows take 78 to 81 us, 5.8 to 6.0 TB/s; one token
+// through the Mixtral-8x7B shaped experts 67 to 69, of which reading the weights is 54.
 //
 // FP8_LINEAR: the halves are 128 output columns each.  FP8_GATED: 128 rows of W_gate and the
 // same 128 of W_up; a thread has one column of h, and a tile's 128 columns are one block of h's
@@ -56,12 +56,14 @@ struct Schedule {
     const int full = total / G, rest = total - full * G;
     // Whole tiles: the last round's `rest` tiles share the memory's rate, but an SM alone still
     // needs 2/5 of the time for a block that it needs when all SMs load.  Cut tiles keep all SMs
-    // loading to the end and cost a join, as long as 4 blocks.  (Two experts' rows, K
-    // = 4096, 148 SMs: N = 20480, 12 left over, 42.0 us whole, 35.6 cut; N = 4096, 32 left over,
-    // 18.8 and 16.6; N = 8192, 64 left over, 20.9 and 21.5; N = 28672, 76 left over, 44.1 and
-    // 45.1.  Seven rounds of 16 experts, 14336 x 4096, 8 left over: 146.9 and 143.2.)  Over many
-    // rounds it gains little, and runs of neighbouring tiles lose that again (27 rounds of the
-    // DeepSeek-shaped decode step: 1588 us and 1603).
+    // loading to the end and cost a join, as long as 4 blocks.  (Two experts' rows, K = 4096, 148
+    // SMs: N = 20480, 12 left over, 42.0 us whole, 35.6 cut; N = 4096, 32 left over, 18.8 and
+    // 16.6; N = 8192, 64 left over, 20.9 and 21.5; N = 28672, 76 left over, 44.1 and 45.1.)  Over
+    // many rounds it gains little, and runs of neighbouring tiles lose that again.  Whole and
+    // cut, us, after `full` whole rounds of 14336 x 4096: 6 rounds 150.7 and 145.8, 9 216.5 and
+    // 213.8, 12 282.0 and 282.4, 15 349.4 and 351.1, 20 461.2 and 459.2, 26 595.3 and 597.5; of
+    // 7168 x 2048: 6 81.5 and 79.4, 9 117.1 and 113.7, 12 150.3 and 150.2, 15 187.4 and 183.6, 20
+    // 242.4 and 239.7, 26 314.1 and 309.1; 27 of the DeepSeek-shaped decode step 1588 and 1603.
     const bool cut = full < 10 && rest != 0 &&
                      static_cast<int64_t>(2 * G - 5 * rest) * KB > 20 * G;
     rounds = cut ? 0 : full + (static_cast<int>(blockIdx.x) < rest ? 1 : 0);

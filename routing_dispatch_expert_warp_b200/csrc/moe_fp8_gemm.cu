@@ -34,18 +34,26 @@
 // A hand-over between an MMA issuer and an epilogue takes some 200 cycles each way.  With the
 // halves apart, four accumulators of 128 columns are on their way round instead of two of 256,
 // and one half's epilogue computes while the other's waits.  (One issuer with MMAs of 256
-// columns for both halves: 115 us for 4096 x 4096 x 7168 and 1.44 ms for the Mixtral-8x7B
-// shaped prefill, against 116.5 and 1.45 here; but 8.1 ms for the DeepSeek-shaped prefill of
-// 16384 tokens against 7.6, and 16.4 us for 13 ragged buckets against 15.6.)
-// What bounds it: the outer sum.  The epilogue adds every block's 128 x 256 partial sums up in
-// fp32 on the general cores, and the card's power limit holds the clock at 1.45 to 1.65 GHz
-// meanwhile: 1.9 to 2.06 PFLOP/s.  Without the epilogue's sums the copies and MMAs run at some
-// 2.5, without the MMAs the sums do as well.  Each instruction of the epilogue's loop counts:
-// its own loads of scales cost a fifth, a warp number that is not known to be uniform 5 to 9%,
-// and four copies of the loop instead of two missed the instruction cache.
-// (Tiles are not cut along the reduction when they are fewer than the SMs: a cut tile's 128 KB
-// of partial sums and their join take as long as 60 to 75 of its blocks.  256 x 4096 x 14336, 32
-// tiles: 60 us whole, 55 cut; 384 x 7168 x 2048: 17 us whole, 41 cut.)
+// columns for both halves, at that step and in bursts: 115 us for 4096 x 4096 x 7168 and 1.44 ms
+// for the Mixtral-8x7B shaped prefill, against 116.5 and 1.45 here; but 8.1 ms for the
+// DeepSeek-shaped prefill of 16384 tokens against 7.6, and 16.4 us for 13 ragged buckets against
+// 15.6.)
+// What it measured: 4096 x 4096 x 7168 in 117 us in a burst after a pause, 2.05 PFLOP/s; back to
+// back for a second 133 to 137, 1.75 to 1.81, as the card's power limit lowers the clock to some
+// 1.58 GHz.  The Mixtral-8x7B shaped prefill of 4096 tokens 1.49 and 1.70 to 1.72 ms (1.42 GHz),
+// the DeepSeek-shaped one of 16384 tokens 7.0 to 7.2 and 8.0 to 8.4 ms (1.30 GHz).
+// What bounds it, beside the power: no unit is full.  In that first case the tensor pipe is busy
+// 61% of the time, the FMA pipe 18%, the issue slots 42%; operands come from L2 at 10 TB/s.  The
+// rest is waiting: for the hand-overs, and in the epilogue for tensor memory, 16 columns at a
+// time with one load in flight.  Without the epilogue's sums the copies and MMAs run at some 2.5
+// PFLOP/s, without the MMAs the sums do as well.  Each instruction of the epilogue's loop
+// counts: its own loads of scales cost a fifth, a warp number that is not known to be uniform 5
+// to 9%, and four copies of the loop instead of two missed the instruction cache.
+// Tiles are not cut along the reduction, so a product of few tiles leaves SMs idle: 128 and 256
+// rows x 4096 x 14336, 16 and 32 tiles, take 51 us, where reading the weight takes 9.  Cutting
+// was tried with a join that stored each lane's sums 512 bytes apart, between fences (256 x 4096
+// x 14336 60 us whole, 55 cut; 384 x 7168 x 2048 17 whole, 41 cut), not with the join of
+// moe_fp8_few.cu.
 // Every wait is bounded as in the bf16 expert GEMM.
 #include "moe_fp8_gemm.cuh"
 
@@ -53,9 +61,14 @@ namespace moe {
 namespace {
 
 constexpr int BM = 128;
-// Mean rows of a bucket up to which moe_fp8_few.cu takes them.  The FFN of 8 experts of 4096 x
-// 14336, few-rows kernel against this one: 32 rows a bucket 248 us against 257, 48 rows 260
-// against 261, 64 rows 329 against 266.
+// Rows an expert of the buffers (the host does not know the buckets) up to which moe_fp8_few.cu
+// takes a product.  That kernel against this one, us, equal buckets that fill the buffers: the
+// FFN of 8 experts of 4096 x 14336, 32 rows a bucket 237 and 258, 64 rows 271 and 272, 96 rows
+// 478 and 279; that of 256 experts of 7168 x 2048, 32 rows 1731 and 1971, 64 rows 1987 and 1986,
+// 96 rows 3734 and 2153; one product of 1 x 4096 x 14336, 32 rows 22 and 49, 64 rows 28 and 50,
+// 256 rows 63 and 51.  So 33 to 64 rows an expert could as well go there, and few tiles should.
+// 256 experts of 2048 x 7168 with 8192 rows, uneven: the longest bucket 267 rows 645 and 661,
+// 1337 rows 702 and 694, 3293 rows 694 and 641.
 constexpr int kFewRows = 32;
 constexpr int A_BYTES = BM * BK;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;

@@ -9,6 +9,7 @@
 #include <mutex>
 #include <string>
 
+#include "moe_fp8.h"
 #include "moe_internal.h"
 
 namespace moe {

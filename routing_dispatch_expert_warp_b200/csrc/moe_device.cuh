@@ -22,8 +22,8 @@ enum DevError : unsigned int {
   DEV_OK = 0,
   DEV_TIMEOUT = 1,
   DEV_BAD_EXPERT = 2,
-  DEV_RECV_OVERFLOW = 3, // an expert-parallel row would land past the receive buffer
-  DEV_BAD_BUCKET = 4     // an fp8 product's bucket reaches outside its rows
+  DEV_RECV_OVERFLOW = 3  // an expert-parallel row would land past the receive buffer
+                         // 4: DEV_BAD_BUCKET (moe_fp8.h)
 };
 
 __device__ __forceinline__ void record_error(DevStatus* st, unsigned int code,
@@ -32,15 +32,6 @@ __device__ __forceinline__ void record_error(DevStatus* st, unsigned int code,
     st->where = where;
     st->info = info;
   }
-}
-
-// Programmatic dependent launch: the blocks of a kernel launched by launch_overlapping may start
-// while the launch before is ending; here they wait until it has completed and its writes are
-// visible (at once when there is nothing to wait for).  It saves 2 us a launch.  Loads of what
-// that launch wrote are plain ones: a read-only load (__ldg, or one through a const __restrict__
-// pointer) promises that nothing writes there while the kernel runs, and may go ahead of the wait.
-__device__ __forceinline__ void wait_for_previous() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 __device__ __forceinline__ uint64_t global_ns() {

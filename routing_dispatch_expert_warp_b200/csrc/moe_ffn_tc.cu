@@ -1436,7 +1436,10 @@ __global__ void __launch_bounds__(256) split_router_weight_kernel(
 }
 
 // ------------------------------------------------------------------ host side
-using EncodeTiledFn = TensorMapEncodeFn;
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 EncodeTiledFn encode_fn() {
   static EncodeTiledFn fn = nullptr;
@@ -1573,8 +1576,6 @@ cudaError_t launch_tokn(const CUtensorMap& tt, const CUtensorMap& tw0, const CUt
 std::atomic<int> g_ffn_kernel{MOE_FFN_TOKEN_MAJOR};
 
 }  // namespace
-
-TensorMapEncodeFn tensor_map_encoder() { return encode_fn(); }
 
 void set_ffn_kernel(int kind) { g_ffn_kernel.store(kind); }
 int ffn_kernel() { return g_ffn_kernel.load(); }

@@ -55,6 +55,8 @@
 // x 14336 60 us whole, 55 cut; 384 x 7168 x 2048 17 whole, 41 cut), not with the join of
 // moe_fp8_few.cu.
 // Every wait is bounded as in the bf16 expert GEMM.
+#include <mutex>
+
 #include "moe_fp8_gemm.cuh"
 
 namespace moe {
@@ -484,6 +486,20 @@ cudaError_t launch(const CUtensorMap& a, const CUtensorMap& a32, const CUtensorM
 }
 
 }  // namespace
+
+TensorMapEncodeFn tensor_map_encoder() {
+  static TensorMapEncodeFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* at = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &at, 12000, cudaEnableDefault,
+                                         &found) == cudaSuccess &&
+        found == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<TensorMapEncodeFn>(at);
+  });
+  return fn;
+}
 
 size_t fp8_workspace_bytes() {
   return kFp8PartialsOffset + sizeof(float) * SLOT_FLOATS * 2 * static_cast<size_t>(sm_count());

@@ -5,7 +5,7 @@
 
 #include <cuda_fp8.h>
 
-#include "moe_internal.h"
+#include "moe_fp8.h"
 
 namespace moe {
 

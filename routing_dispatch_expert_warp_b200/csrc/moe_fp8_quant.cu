@@ -29,7 +29,7 @@
 // 144), of fp32 6.3 to 6.6 (93 and 202 us).
 #include <cuda_fp8.h>
 
-#include "moe_internal.h"
+#include "moe_fp8.h"
 
 namespace moe {
 namespace {

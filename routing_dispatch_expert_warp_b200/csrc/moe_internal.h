@@ -164,50 +164,6 @@ cudaError_t launch_ep_stats(const Shape& s, const int32_t* mat, const int32_t* e
                             int world, int ranks_per_node, moe_ep_stats_t* out,
                             cudaStream_t st);
 
-// 8-bit floating point (moe_fp8_quant.cu, moe_fp8_gemm.cu): see include/moe.h.
-cudaError_t launch_fp8_quantize_rows(int dtype, const void* x, int64_t rows_in, int64_t cols,
-                                     const int32_t* assign_row, int k, int64_t rows_out,
-                                     void* q, float* scale, cudaStream_t st);
-cudaError_t launch_fp8_quantize_weights(int dtype, const void* w, int64_t E, int64_t n,
-                                        int64_t cols, void* q, float* scale, cudaStream_t st);
-// One grouped product: out (w1 == nullptr), or h and h_scale of the gate (w0) and up (w1)
-// weights.  Sizes checked by the caller.
-struct Fp8Gemm {
-  int E;
-  int64_t rows, N, K;
-  const void* a;            // [rows, K]
-  const float* a_scale;     // [rows, ceil(K / 128)]
-  const int32_t* seg_start; // [E]
-  const int32_t* seg_count; // [E]
-  const void* w0;           // [E, N, K]
-  const float* w_scale0;    // [E, ceil(N / 128), ceil(K / 128)]
-  const void* w1;
-  const float* w_scale1;
-  void* out;                // [rows, N] bf16
-  void* h;                  // [rows, N] e4m3
-  float* h_scale;           // [rows, ceil(N / 128)]
-  bool follows;             // the launch before in the stream is the product that made a: only
-                            // a and a_scale depend on it
-};
-// Most rows of a product: rounded up to whole tiles of 128 they still fit in an int.
-constexpr int64_t kFp8MaxRows = 2147483647LL - 127;
-// Most tiles of a product: so does a block's step past the last one.
-constexpr int64_t kFp8MaxTiles = 2147483647LL - 65535;
-// Workspace of the fp8 products: the status record, then arrival counters (zero between
-// calls), then partial sums.
-constexpr size_t kFp8CountersOffset = 256;
-constexpr size_t kFp8PartialsOffset = 4096;
-size_t fp8_workspace_bytes();
-cudaError_t launch_fp8_gemm(const Fp8Gemm& g, void* ws, uint64_t wait_ns, cudaStream_t st,
-                            const char** why);
-
-// cuTensorMapEncodeTiled of the driver (nullptr: not available).
-using TensorMapEncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                       const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                       const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                       CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-TensorMapEncodeFn tensor_map_encoder();
-
 // Which kernel runs the expert FFN of the plain (permuted-copy) path, process-wide: a
 // moe_ffn_kernel_t value (include/moe.h).
 void set_ffn_kernel(int kind);
@@ -215,26 +171,6 @@ int ffn_kernel();
 
 // Process-wide count of this library's kernel launches (every launch site calls it once).
 void note_launch();
-
-// A launch whose blocks may start while the launch before in the stream is ending: each begins
-// with wait_for_previous() (moe_device.cuh).
-template <typename... Params, typename... Args>
-cudaError_t launch_overlapping(void (*kernel)(Params...), int64_t blocks, int threads, int smem,
-                               cudaStream_t st, const Args&... args) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, args...);
-  if (err == cudaSuccess) note_launch();
-  return err;
-}
 
 // Allocation-free dispatch: scratch lives in a fixed device array (moe_dispatch.cu).
 constexpr size_t kStaticDispatchHistBytes = size_t(1) << 20;  // 1 MiB of block histograms

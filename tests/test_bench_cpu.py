@@ -156,3 +156,14 @@ def test_route_tensor_roof_only_for_the_tensor_core_router():
         assert not bench.tensor_core_router(shape)
         assert bench.route_tensor_roof(shape, bench.algorithmic_work(shape, 1), 0.2, peaks) == {}
     assert bench.tensor_core_router(ds.replace(E=33))
+
+
+def test_the_recorded_traffic_is_not_voided_by_other_kernels():
+    """The record holds for the code of the bf16 grouped GEMM's files: what the 8-bit kernels share
+    stands in files of its own."""
+    import os
+    for rel in bench.GEMM_SOURCES:
+        with open(os.path.join(os.path.dirname(os.path.abspath(bench.__file__)), rel)) as f:
+            code = bench._code_only(f.read()).lower()
+        for word in ("fp8", "wait_for_previous", "launch_overlapping", "tensor_map_encoder"):
+            assert word not in code, (rel, word)

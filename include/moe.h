@@ -567,9 +567,10 @@ moe_status_t moe_layer_forward(const moe_config_t* cfg, const moe_layer_inputs_t
  *   gets scale NaN and NaN in every entry.
  *
  * Row widths (cols, K, d_model, d_ff) are multiples of 16 up to 2^24; pointers are 16-byte
- * aligned.  dtype is the element type of x or w (MOE_F32 or MOE_BF16). */
+ * aligned.  dtype is the element type of x or w (MOE_F32 or MOE_BF16).  No output of these calls
+ * may share memory with an input or another output. */
 
-/* Rows in place: q and scale of row r in row r.  rows = 0 does nothing.  One kernel. */
+/* Row by row: q and scale of row r of x in row r.  rows = 0 does nothing.  One kernel. */
 moe_status_t moe_fp8_quantize_rows(int32_t dtype, int64_t rows, int64_t cols, const void* x,
                                    void* q, float* scale, void* stream);
 

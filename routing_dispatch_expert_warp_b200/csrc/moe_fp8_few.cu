@@ -5,7 +5,7 @@
 // 128 places, 4 rows cost the tensor cores and the epilogue as much as 128 (and power, which the
 // clocks pay for): a DeepSeek-shaped decode step of 4 rows an expert takes 2.08 ms there and 1.60
 // to 1.68 here, where a block of 128 costs the epilogue 16 sums a thread; that is 6.6 to 6.9
-// TB/s.  32 experts of 7168 x 2048 with 128 rows take 78 to 81 us, 5.8 to 6.0 TB/s; one token
+// TB/s.  32 experts of 7168 x 2048 with 128 rows take 77 to 81 us, 5.8 to 6.1 TB/s; one token
 // through the Mixtral-8x7B shaped experts 67 to 69, of which reading the weights is 54.
 //
 // FP8_LINEAR: the halves are 128 output columns each.  FP8_GATED: 128 rows of W_gate and the
